@@ -217,7 +217,7 @@ def _quantise(x):
     x = x.float()
     lo, hi = x.amin(-1).clamp(max=0.0), x.amax(-1).clamp(min=0.0)
     span = hi - lo
-    s = (span / 15.0).bfloat16().float()
+    s = (span / torch.full_like(span, 15.0)).bfloat16().float()  # (a scalar divisor would be a product)
     none = s < 2.0 ** -126
     r = 1.0 / s
     z = torch.where(none, torch.zeros_like(s), torch.round(-lo * r))
