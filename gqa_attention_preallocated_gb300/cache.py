@@ -17,13 +17,48 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import KVC_BF16, KVC_F32, KVC_FP8_E4M3, KVCError, check, lib
+from ._lib import KVC_BF16, KVC_F32, KVC_FP8_E4M3, KVC_Q4, KVCError, check, lib
 
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _I64P = ctypes.POINTER(ctypes.c_int64)
 
-# storage dtype -> library dtype; an FP8 E4M3 cache takes bf16 q / k_new / v_new / out
-_DTYPES = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float8_e4m3fn: KVC_FP8_E4M3}
+# storage dtype -> library dtype; FP8 E4M3 and 4-bit ("q4") caches take bf16 q / k_new / v_new / out
+_DTYPES = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16, torch.float8_e4m3fn: KVC_FP8_E4M3, "q4": KVC_Q4}
+
+
+def _io_dtype(dtype) -> torch.dtype:
+    return torch.float32 if dtype == torch.float32 else torch.bfloat16
+
+
+def _buffers(given, layers: int, shape, dtype: torch.dtype, device: torch.device, name: str) -> list:
+    """One buffer a layer: the caller's, checked, or new ones."""
+    if given is None:
+        return [torch.empty(shape, dtype=dtype, device=device) for _ in range(layers)]
+    bufs = list(given)
+    for t in bufs:
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+            raise KVCError(1, f"{name} must be contiguous {tuple(shape)} {dtype}")
+    return bufs
+
+
+def _layer_buffers(dtype, layers: int, head, d: int, device, k_bufs, v_bufs, k_scales, v_scales):
+    """(k, v, k_scale, v_scale) buffer lists: rows [*head, d] of ``dtype``, or for 4-bit caches codes
+    [*head, d / 2] uint8 and scale words int32 [*head[:-1], head[-1] rounded up to a multiple of 4]."""
+    if dtype != "q4":
+        if k_scales is not None or v_scales is not None:
+            raise KVCError(1, "scale buffers belong to 4-bit caches")
+        shape = (*head, d)
+        return (_buffers(k_bufs, layers, shape, dtype, device, "cache buffers"),
+                _buffers(v_bufs, layers, shape, dtype, device, "cache buffers"), None, None)
+    codes, words = (*head, d // 2), (*head[:-1], -(-head[-1] // 4) * 4)
+    return (_buffers(k_bufs, layers, codes, torch.uint8, device, "code buffers"),
+            _buffers(v_bufs, layers, codes, torch.uint8, device, "code buffers"),
+            _buffers(k_scales, layers, words, torch.int32, device, "scale buffers"),
+            _buffers(v_scales, layers, words, torch.int32, device, "scale buffers"))
+
+
+def _pointers(bufs) -> ctypes.Array:
+    return (ctypes.c_void_p * len(bufs))(*[t.data_ptr() for t in bufs])
 
 
 def _stream_ptr(device: torch.device, stream=None) -> int:
@@ -52,32 +87,35 @@ class KVCache:
     ``k_bufs`` / ``v_bufs`` may be given (lists of contiguous CUDA tensors of
     that shape); otherwise they are allocated here with ``torch.empty``.  The
     handle borrows them; this object keeps them alive.
+
+    ``dtype="q4"`` holds K and V in 4 bits, with a step and a zero point for
+    every row (token and KV head) that appends choose: ``k`` / ``v`` are then
+    uint8 codes [B, Hkv, max_len, d / 2] and ``k_scale`` / ``v_scale`` int32
+    words [B, Hkv, max_len rounded up to a multiple of 4]; inputs and outputs
+    are bf16 (the format is in ``include/kvc.h``, kvc_create_quantized).
     """
 
     def __init__(self, layers: int, batch: int, kv_heads: int, max_len: int, head_dim: int,
-                 dtype: torch.dtype = torch.bfloat16, device="cuda", k_bufs=None, v_bufs=None):
+                 dtype=torch.bfloat16, device="cuda", k_bufs=None, v_bufs=None, k_scales=None, v_scales=None):
         if dtype not in _DTYPES:
             raise KVCError(1, f"unsupported dtype {dtype}")
         self.layers, self.B, self.Hkv, self.max_len, self.d = layers, batch, kv_heads, max_len, head_dim
         self.dtype = dtype
-        self.io_dtype = torch.bfloat16 if dtype == torch.float8_e4m3fn else dtype
+        self.io_dtype = _io_dtype(dtype)
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
-        shape = (batch, kv_heads, max_len, head_dim)
-        if k_bufs is None:
-            k_bufs = [torch.empty(shape, dtype=dtype, device=self.device) for _ in range(layers)]
-        if v_bufs is None:
-            v_bufs = [torch.empty(shape, dtype=dtype, device=self.device) for _ in range(layers)]
-        for t in list(k_bufs) + list(v_bufs):
-            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-                raise KVCError(1, f"cache buffers must be contiguous {shape} {dtype}")
-        self.k, self.v = list(k_bufs), list(v_bufs)
-        kp = (ctypes.c_void_p * layers)(*[t.data_ptr() for t in self.k])
-        vp = (ctypes.c_void_p * layers)(*[t.data_ptr() for t in self.v])
+        self.k, self.v, self.k_scale, self.v_scale = _layer_buffers(
+            dtype, layers, (batch, kv_heads, max_len), head_dim, self.device, k_bufs, v_bufs, k_scales, v_scales)
         h = ctypes.c_void_p()
-        check(lib().kvc_create(ctypes.byref(h), layers, batch, kv_heads, max_len, head_dim, _DTYPES[dtype], kp, vp))
+        if dtype == "q4":
+            check(lib().kvc_create_quantized(ctypes.byref(h), layers, batch, kv_heads, max_len, head_dim,
+                                             _pointers(self.k), _pointers(self.v), _pointers(self.k_scale),
+                                             _pointers(self.v_scale)))
+        else:
+            check(lib().kvc_create(ctypes.byref(h), layers, batch, kv_heads, max_len, head_dim, _DTYPES[dtype],
+                                   _pointers(self.k), _pointers(self.v)))
         self._h = h
         self._ws = None
         self._dev_lens = None
@@ -167,6 +205,32 @@ class KVCache:
         nn = _i32(n_new, self.B)
         check(lib().kvc_append(self._h, layer, _ptr(k_new), _ptr(v_new), T, nn.ctypes.data_as(_I32P),
                                _stream_ptr(self.device, stream)))
+
+    def read(self, layer: int, first, count, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+             stream=None):
+        """Rows read back: positions first[b] .. first[b] + count[b] - 1 of row b, as (k, v) [B, Hkv, T, d].
+
+        ``k_out`` / ``v_out`` (both or neither) fix T and keep what they hold
+        at t >= count[b]; without them T is the largest count and those entries
+        are zeros.  A 4-bit or FP8 cache's values come rounded to bf16.
+        """
+        fa = np.ascontiguousarray(np.asarray(first, dtype=np.int64).reshape(-1))
+        if fa.shape[0] != self.B:
+            raise KVCError(1, f"expected {self.B} first positions, got {fa.shape[0]}")
+        cn = _i32(count, self.B)
+        if (k_out is None) != (v_out is None):
+            raise KVCError(1, "k_out and v_out come together")
+        if k_out is None:
+            T = max(0, int(cn.max())) if self.B else 0
+            with torch.cuda.stream(stream):  # (None: the current one) so that the zeros are there first
+                k_out = torch.zeros((self.B, self.Hkv, T, self.d), dtype=self.io_dtype, device=self.device)
+                v_out = torch.zeros_like(k_out)
+        T = k_out.shape[2] if k_out.dim() == 4 else -1
+        self._check_tensor(k_out, (self.B, self.Hkv, T, self.d), "k_out")
+        self._check_tensor(v_out, (self.B, self.Hkv, T, self.d), "v_out")
+        check(lib().kvc_read(self._h, layer, fa.ctypes.data_as(_I64P), cn.ctypes.data_as(_I32P), T, _ptr(k_out),
+                             _ptr(v_out), _stream_ptr(self.device, stream)))
+        return k_out, v_out
 
     def gqa_attention(self, layer: int, q: torch.Tensor, n_new, out: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -359,11 +423,13 @@ class PagedKVCache(KVCache):
     this object) maps row b's logical page i to a physical page; it starts as
     row b owning pages b * max_pages_per_row .. (as long as num_pages allows,
     else -1) and may be rewritten between calls.  Every call works on the
-    logical sequence, with max_len = max_pages_per_row * page_size.
+    logical sequence, with max_len = max_pages_per_row * page_size.  With
+    ``dtype="q4"`` the pages hold codes and ``k_scale`` / ``v_scale`` their
+    scale words, as in ``KVCache``.
     """
 
     def __init__(self, layers: int, batch: int, kv_heads: int, page_size: int, num_pages: int,
-                 max_pages_per_row: int, head_dim: int, dtype: torch.dtype = torch.bfloat16, device="cuda"):
+                 max_pages_per_row: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
         if dtype not in _DTYPES:
             raise KVCError(1, f"unsupported dtype {dtype}")
         dev = torch.device(device)
@@ -373,18 +439,21 @@ class PagedKVCache(KVCache):
         self.page_size, self.num_pages, self.max_pages_per_row = page_size, num_pages, max_pages_per_row
         self.max_len = max_pages_per_row * page_size
         self.dtype, self.device = dtype, dev
-        self.io_dtype = torch.bfloat16 if dtype == torch.float8_e4m3fn else dtype
-        shape = (num_pages, kv_heads, page_size, head_dim)
-        self.k = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(layers)]
-        self.v = [torch.empty(shape, dtype=dtype, device=dev) for _ in range(layers)]
+        self.io_dtype = _io_dtype(dtype)
+        self.k, self.v, self.k_scale, self.v_scale = _layer_buffers(
+            dtype, layers, (num_pages, kv_heads, page_size), head_dim, dev, None, None, None, None)
         ids = torch.arange(batch * max_pages_per_row, dtype=torch.int32, device=dev)
         self.block_table = torch.where(ids < num_pages, ids, torch.full_like(ids, -1)).view(batch, max_pages_per_row)
-        kp = (ctypes.c_void_p * layers)(*[t.data_ptr() for t in self.k])
-        vp = (ctypes.c_void_p * layers)(*[t.data_ptr() for t in self.v])
         h = ctypes.c_void_p()
-        check(lib().kvc_create_paged(ctypes.byref(h), layers, batch, kv_heads, page_size, num_pages,
-                                     max_pages_per_row, head_dim, _DTYPES[dtype], kp, vp,
-                                     self.block_table.data_ptr()))
+        if dtype == "q4":
+            check(lib().kvc_create_quantized_paged(ctypes.byref(h), layers, batch, kv_heads, page_size, num_pages,
+                                                   max_pages_per_row, head_dim, _pointers(self.k), _pointers(self.v),
+                                                   _pointers(self.k_scale), _pointers(self.v_scale),
+                                                   self.block_table.data_ptr()))
+        else:
+            check(lib().kvc_create_paged(ctypes.byref(h), layers, batch, kv_heads, page_size, num_pages,
+                                         max_pages_per_row, head_dim, _DTYPES[dtype], _pointers(self.k),
+                                         _pointers(self.v), self.block_table.data_ptr()))
         self._h = h
         self._ws = None
         self._dev_lens = None

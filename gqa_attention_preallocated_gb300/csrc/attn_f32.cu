@@ -1,6 +1,6 @@
 // Generic GQA attention: fp32 storage (d <= 256, d % 4 == 0), and bf16
 // storage of a head dimension other than the 128 the TMA / tensor-core
-// kernels take (d <= 256, d % 8 == 0).  Values are widened to fp32 as they
+// kernels take (d <= 256, d % 8 == 0), FP8 and 4-bit storage.  Values are widened to fp32 as they
 // are staged in shared memory; scores, softmax and the output accumulate in
 // fp32; a bf16 cache takes bf16 queries and writes bf16 outputs (rounded to
 // nearest even).
@@ -35,6 +35,7 @@
 
 #include "kvc_internal.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 
 namespace kvc {
 
@@ -118,11 +119,26 @@ __device__ __forceinline__ void stage16_rows(float* dst, const __nv_bfloat16* sr
     }
 }
 
-// SE: the stored type (float, bf16, or E4M3 codes as uint8_t); IE: the type
-// of the queries and outputs.
+// 4-bit rows: 16 bytes hold 32 codes; value = s * (c - z), exact in fp32 (an
+// 8-bit step times a 5-bit integer).
+struct Q4Byte {
+    uint8_t two_codes;
+};
+__device__ __forceinline__ void stage_q4(float* dst, const Q4Byte* src, uint32_t scale_word) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const float s = q4::step_of(scale_word);
+    const int z = q4::zero_of(scale_word);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) dst[i] = s * static_cast<float>(q4::code_of(u[i >> 3], i & 7) - z);
+}
+
+// SE: the stored type (float, bf16, E4M3 codes as uint8_t, or pairs of 4-bit
+// codes); IE: the type of the queries and outputs.
 template <typename SE, typename IE>
 __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_constant__ F32Params p) {
-    constexpr int kVec = 16 / static_cast<int>(sizeof(SE));  // values per 16-byte load
+    constexpr bool kQ4 = std::is_same<SE, Q4Byte>::value;
+    constexpr int kVec = kQ4 ? 32 : 16 / static_cast<int>(sizeof(SE));  // values per 16-byte load
     constexpr bool kF8 = std::is_same<SE, uint8_t>::value;
     const IE* qg = static_cast<const IE*>(p.q);
     const SE* kg = static_cast<const SE*>(p.k_cache);
@@ -190,18 +206,27 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
         for (int idx = threadIdx.x; idx < kKeys * d / kVec; idx += blockDim.x) {
             const int j = (idx * kVec) / d;
             bool live = false;
-            size_t off = 0;
+            size_t off = 0, sidx = 0;
             if (j < nk) {
                 const int a = k0 + j;  // key position
                 bool bad = false;
                 const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, kvh, a, &bad);
                 live = !bad;  // a bad block-table entry reads as zeros
                 off = static_cast<size_t>(row) * d + static_cast<size_t>(idx * kVec - j * d);
+                if constexpr (kQ4) {
+                    off /= 2;  // two codes a byte
+                    sidx = q4::scale_index(p.q4, row);
+                }
             }
             float* kdst = sk + j * dk + (idx * kVec - j * d);
             if (live) {
-                stage16_rows(kdst, kg + off, ksc);
-                stage16(sv + idx * kVec, vg + off, vsc);
+                if constexpr (kQ4) {
+                    stage_q4(kdst, kg + off, __ldg(p.q4.k + sidx));
+                    stage_q4(sv + idx * kVec, vg + off, __ldg(p.q4.v + sidx));
+                } else {
+                    stage16_rows(kdst, kg + off, ksc);
+                    stage16(sv + idx * kVec, vg + off, vsc);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) kdst[i] = sv[idx * kVec + i] = 0.f;
@@ -255,6 +280,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
             const int jmax = min(nk, li - k0 + 1);
             for (int j = max(0, lo - k0 + 1); j < jmax; ++j) {
                 const float pb = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
+                // (4-bit rows: a draft token off the query's path may be a NaN row)
+                if (kQ4 && p.tree && __shfl_sync(0xffffffffu, j < 32 ? sc[0] : sc[1], j & 31) == -INFINITY) continue;
                 const float* vr = sv + j * d;
 #pragma unroll
                 for (int c = 0; c < kMaxD / 32; ++c) {
@@ -359,6 +386,7 @@ cudaError_t launch_generic(const F32Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_attn_f32(const F32Params& p, cudaStream_t stream) {
+    if (p.kind == 3) return launch_generic<Q4Byte, __nv_bfloat16>(p, stream);
     if (p.kind == 2) return launch_generic<uint8_t, __nv_bfloat16>(p, stream);
     if (p.kind == 1) return launch_generic<__nv_bfloat16, __nv_bfloat16>(p, stream);
     return launch_generic<float, float>(p, stream);

@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <queue>
 #include <string>
 #include <vector>
@@ -36,6 +37,8 @@ struct kvc_cache {
     // FP8 E4M3 caches: K and V scale of every (layer, KV head), [layers * Hkv]
     std::vector<float> kscale, vscale;
     std::vector<void*> k, v;
+    // 4-bit caches: the scale words' buffers
+    std::vector<void*> ks, vs;
     std::vector<int64_t> lens;  // [layers * B]
     // device state, set up on first launch
     bool dev_ready = false;
@@ -86,7 +89,8 @@ int tc_min_rows(const kvc_cache* c) { return c->dtype == KVC_FP8_E4M3 ? kTcMinRo
 // bf16 or FP8 storage whose head dimension has no TMA kernel (the split-KV
 // kernel takes d = 128, and d = 64 for bf16; the tensor-core kernel d = 128).
 bool generic_path(const kvc_cache* c) {
-    return c->dtype == KVC_F32 || !(c->d == kHeadDimBf16 || (c->d == kHeadDimSmall && c->dtype == KVC_BF16));
+    return c->dtype == KVC_F32 || c->dtype == KVC_Q4 ||
+           !(c->d == kHeadDimBf16 || (c->d == kHeadDimSmall && c->dtype == KVC_BF16));
 }
 // Head dimension the tensor-core kernel is built for.
 bool tc_capable(const kvc_cache* c) { return !generic_path(c) && c->d == kHeadDimBf16; }
@@ -345,6 +349,20 @@ kvc_status validate_attention(const kvc_cache* c, int layer, const void* q, int 
 // Launches (arguments already validated)
 // ---------------------------------------------------------------------------
 
+// Bytes of one element of q, k_new, v_new and out (bf16 for an FP8 or 4-bit cache).
+size_t io_esize(const kvc_cache* c) { return c->dtype == KVC_F32 ? 4 : 2; }
+
+// A 4-bit cache's scale words (null pointers for the other types).
+Q4Scales q4_scales(const kvc_cache* c, int layer) {
+    Q4Scales s{nullptr, nullptr, 0, 0};
+    if (c->dtype != KVC_Q4) return s;
+    s.k = static_cast<uint32_t*>(c->ks[layer]);
+    s.v = static_cast<uint32_t*>(c->vs[layer]);
+    s.tokens = c->pg.table ? c->pg.page : c->max_len;
+    s.stride = (s.tokens + 3) / 4 * 4;
+    return s;
+}
+
 // The layer's FP8 scales into a split-KV parameter block (no-op for bf16).
 void set_decode_scales(const kvc_cache* c, int layer, DecodeParams* p) {
     if (c->dtype != KVC_FP8_E4M3) return;
@@ -368,7 +386,8 @@ kvc_status do_append(kvc_cache* c, int layer, const void* k_new, const void* v_n
     p.T = T;
     p.max_len = c->max_len;
     p.fp8 = c->dtype == KVC_FP8_E4M3 ? 1 : 0;
-    p.row_bytes = c->d * (p.fp8 ? 2 : c->esize);  // source rows (bf16 for an FP8 cache)
+    p.row_bytes = c->d * static_cast<int>(io_esize(c));  // source rows (bf16 for an FP8 or 4-bit cache)
+    p.q4 = q4_scales(c, layer);
     p.ring = c->ring ? 1 : 0;
     p.pg = c->pg;
     if (p.fp8)
@@ -381,7 +400,7 @@ kvc_status do_append(kvc_cache* c, int layer, const void* k_new, const void* v_n
         p.lens[b] = static_cast<int>(lens[b]);
         p.n_new[b] = n_new[b];
     }
-    cudaError_t e = launch_append(p, max_n, stream);
+    cudaError_t e = c->dtype == KVC_Q4 ? launch_append_q4(p, max_n, stream) : launch_append(p, max_n, stream);
     if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
     ++c->launches;
     return ok();
@@ -403,7 +422,8 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         p.k_cache = c->k[layer];
         p.v_cache = c->v[layer];
         p.out = out;
-        p.kind = c->dtype == KVC_FP8_E4M3 ? 2 : (c->dtype == KVC_BF16 ? 1 : 0);
+        p.kind = c->dtype == KVC_Q4 ? 3 : c->dtype == KVC_FP8_E4M3 ? 2 : (c->dtype == KVC_BF16 ? 1 : 0);
+        p.q4 = q4_scales(c, layer);
         for (int h = 0; h < c->Hkv && p.kind == 2; ++h) {
             p.kscale[h] = c->kscale[static_cast<size_t>(layer) * c->Hkv + h];
             p.vscale[h] = c->vscale[static_cast<size_t>(layer) * c->Hkv + h];
@@ -852,9 +872,6 @@ kvc_status check_host_lens(const kvc_cache* c) {
 // Helpers of the host-buffer calls (kvc_append_attention_host).
 namespace {
 
-// Bytes of one element of q, k_new, v_new and out (bf16 for an FP8 cache).
-size_t io_esize(const kvc_cache* c) { return c->dtype == KVC_FP8_E4M3 ? 2 : static_cast<size_t>(c->esize); }
-
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Streams, events and two staging slots of at least `bytes` each.  A slot that
@@ -925,19 +942,16 @@ cudaError_t copy_chunk(void* dst, const void* src, int B, int H, int T, size_t r
 
 }  // namespace
 
-extern "C" {
-
-kvc_status kvc_create(kvc_cache** out, int layers, int batch, int kv_heads, int max_len, int head_dim,
-                      kvc_dtype dtype, void* const* k_bufs, void* const* v_bufs) {
-    if (!out) return fail(KVC_ERR_ARG, "out is null");
-    *out = nullptr;
+// kvc_create for every storage type (k_scales / v_scales: 4-bit caches only).
+static kvc_status create_impl(kvc_cache** out, int layers, int batch, int kv_heads, int max_len, int head_dim,
+                              kvc_dtype dtype, void* const* k_bufs, void* const* v_bufs, void* const* k_scales,
+                              void* const* v_scales) {
     if (layers < 1 || batch < 0 || kv_heads < 1 || max_len < 1 || head_dim < 1)
         return fail(KVC_ERR_ARG, "bad geometry: layers=%d batch=%d kv_heads=%d max_len=%d head_dim=%d", layers, batch,
                     kv_heads, max_len, head_dim);
     if (batch > KVC_MAX_BATCH) return fail(KVC_ERR_ARG, "batch %d > %d", batch, KVC_MAX_BATCH);
-    if (dtype != KVC_F32 && dtype != KVC_BF16 && dtype != KVC_FP8_E4M3)
-        return fail(KVC_ERR_ARG, "unknown dtype %d", static_cast<int>(dtype));
     const int esize = dtype == KVC_F32 ? 4 : (dtype == KVC_BF16 ? 2 : 1);
+    if (dtype == KVC_Q4 && head_dim % 32 != 0) return fail(KVC_ERR_ARG, "4-bit caches take a head_dim that is a multiple of 32");
     if ((head_dim * esize) % 16 != 0) return fail(KVC_ERR_ARG, "head_dim * element size must be a multiple of 16");
     if (head_dim > 256) return fail(KVC_ERR_ARG, "head_dim %d > 256", head_dim);
     if (dtype == KVC_FP8_E4M3 && kv_heads > kMaxScaleHeads)
@@ -950,6 +964,14 @@ kvc_status kvc_create(kvc_cache** out, int layers, int batch, int kv_heads, int 
         if (!aligned16(k_bufs[l]) || !aligned16(v_bufs[l]))
             return fail(KVC_ERR_ARG, "layer %d buffer not 16-byte aligned", l);
     }
+    if (dtype == KVC_Q4) {
+        if (!k_scales || !v_scales) return fail(KVC_ERR_ARG, "k_scales / v_scales is null");
+        for (int l = 0; l < layers; ++l) {
+            if (!k_scales[l] || !v_scales[l]) return fail(KVC_ERR_ARG, "layer %d scale buffer is null", l);
+            if (!aligned16(k_scales[l]) || !aligned16(v_scales[l]))
+                return fail(KVC_ERR_ARG, "layer %d scale buffer not 16-byte aligned", l);
+        }
+    }
     kvc_cache* c = new kvc_cache;
     c->layers = layers;
     c->B = batch;
@@ -960,6 +982,10 @@ kvc_status kvc_create(kvc_cache** out, int layers, int batch, int kv_heads, int 
     c->esize = esize;
     c->k.assign(k_bufs, k_bufs + layers);
     c->v.assign(v_bufs, v_bufs + layers);
+    if (dtype == KVC_Q4) {
+        c->ks.assign(k_scales, k_scales + layers);
+        c->vs.assign(v_scales, v_scales + layers);
+    }
     c->lens.assign(static_cast<size_t>(layers) * batch, 0);
     c->tmK.resize(layers);
     c->tmV.resize(layers);
@@ -970,6 +996,29 @@ kvc_status kvc_create(kvc_cache** out, int layers, int batch, int kv_heads, int 
     c->vscale.assign(static_cast<size_t>(layers) * kv_heads, 1.0f);
     *out = c;
     return ok();
+}
+
+extern "C" {
+
+kvc_status kvc_create(kvc_cache** out, int layers, int batch, int kv_heads, int max_len, int head_dim,
+                      kvc_dtype dtype, void* const* k_bufs, void* const* v_bufs) {
+    if (!out) return fail(KVC_ERR_ARG, "out is null");
+    *out = nullptr;
+    if (dtype != KVC_F32 && dtype != KVC_BF16 && dtype != KVC_FP8_E4M3)
+        return fail(KVC_ERR_ARG, "unknown dtype %d%s", static_cast<int>(dtype),
+                    dtype == KVC_Q4 ? " (4-bit caches: kvc_create_quantized)" : "");
+    return create_impl(out, layers, batch, kv_heads, max_len, head_dim, dtype, k_bufs, v_bufs, nullptr, nullptr);
+}
+
+kvc_status kvc_create_quantized(kvc_cache** out, int layers, int batch, int kv_heads, int max_len, int head_dim,
+                         void* const* k_bufs, void* const* v_bufs, void* const* k_scales, void* const* v_scales) {
+    if (!out) return fail(KVC_ERR_ARG, "out is null");
+    *out = nullptr;
+    try {
+        return create_impl(out, layers, batch, kv_heads, max_len, head_dim, KVC_Q4, k_bufs, v_bufs, k_scales, v_scales);
+    } catch (const std::bad_alloc&) {
+        return fail(KVC_ERR_ARG, "out of host memory for a cache of %d layers", layers);
+    }
 }
 
 kvc_status kvc_set_kv_scales(kvc_cache* c, int layer, const float* k_scale, const float* v_scale) {
@@ -989,14 +1038,19 @@ kvc_status kvc_set_kv_scales(kvc_cache* c, int layer, const float* k_scale, cons
     return ok();
 }
 
-kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads, int page_size, int num_pages,
-                            int max_pages_per_row, int head_dim, kvc_dtype dtype, void* const* k_bufs,
-                            void* const* v_bufs, const int32_t* block_table) {
+// kvc_create_paged for every storage type (k_scales / v_scales: 4-bit caches only).
+static kvc_status create_paged_impl(kvc_cache** out, int layers, int batch, int kv_heads, int page_size, int num_pages,
+                                    int max_pages_per_row, int head_dim, kvc_dtype dtype, void* const* k_bufs,
+                                    void* const* v_bufs, void* const* k_scales, void* const* v_scales,
+                                    const int32_t* block_table) {
     if (!out) return fail(KVC_ERR_ARG, "out is null");
     *out = nullptr;
     if (page_size < 1 || num_pages < 1 || max_pages_per_row < 1)
         return fail(KVC_ERR_ARG, "bad paging: page_size=%d num_pages=%d max_pages_per_row=%d", page_size, num_pages,
                     max_pages_per_row);
+    if (dtype == KVC_Q4 && (head_dim == kHeadDimBf16 || head_dim == kHeadDimSmall) && page_size % 128 != 0)
+        return fail(KVC_ERR_ARG, "4-bit pages of head_dim %d and %d hold a multiple of 128 tokens (key tiles never cross a page)",
+                    kHeadDimSmall, kHeadDimBf16);
     if (dtype != KVC_F32 && head_dim == kHeadDimBf16 && page_size % 128 != 0)
         return fail(KVC_ERR_ARG, "bf16 and fp8 pages of head_dim %d hold a multiple of 128 tokens (key tiles never cross a page)",
                     kHeadDimBf16);
@@ -1012,10 +1066,31 @@ kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads
     if (static_cast<long long>(batch) * max_pages_per_row >= (1ll << 31))
         return fail(KVC_ERR_ARG, "batch * max_pages_per_row too large");
     // The ordinary handle over the logical geometry; the buffers are pages.
-    kvc_status s = kvc_create(out, layers, batch, kv_heads, static_cast<int>(cap), head_dim, dtype, k_bufs, v_bufs);
+    kvc_status s = dtype == KVC_Q4
+                       ? kvc_create_quantized(out, layers, batch, kv_heads, static_cast<int>(cap), head_dim, k_bufs, v_bufs,
+                                       k_scales, v_scales)
+                       : kvc_create(out, layers, batch, kv_heads, static_cast<int>(cap), head_dim, dtype, k_bufs, v_bufs);
     if (s) return s;
     (*out)->pg = Paging{block_table, page_size, max_pages_per_row, num_pages};
     return ok();
+}
+
+kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads, int page_size, int num_pages,
+                            int max_pages_per_row, int head_dim, kvc_dtype dtype, void* const* k_bufs,
+                            void* const* v_bufs, const int32_t* block_table) {
+    if (out && dtype == KVC_Q4) {
+        *out = nullptr;
+        return fail(KVC_ERR_ARG, "unknown dtype %d (4-bit caches: kvc_create_quantized_paged)", static_cast<int>(dtype));
+    }
+    return create_paged_impl(out, layers, batch, kv_heads, page_size, num_pages, max_pages_per_row, head_dim, dtype,
+                             k_bufs, v_bufs, nullptr, nullptr, block_table);
+}
+
+kvc_status kvc_create_quantized_paged(kvc_cache** out, int layers, int batch, int kv_heads, int page_size, int num_pages,
+                               int max_pages_per_row, int head_dim, void* const* k_bufs, void* const* v_bufs,
+                               void* const* k_scales, void* const* v_scales, const int32_t* block_table) {
+    return create_paged_impl(out, layers, batch, kv_heads, page_size, num_pages, max_pages_per_row, head_dim, KVC_Q4,
+                             k_bufs, v_bufs, k_scales, v_scales, block_table);
 }
 
 void kvc_destroy(kvc_cache* c) {
@@ -1050,6 +1125,62 @@ kvc_status kvc_append(kvc_cache* c, int layer, const void* k_new, const void* v_
     }
     int64_t* lens = c->lens.data() + static_cast<size_t>(layer) * c->B;
     for (int b = 0; b < c->B; ++b) lens[b] += n_new[b];
+    return ok();
+}
+
+kvc_status kvc_read(kvc_cache* c, int layer, const int64_t* first, const int32_t* count, int T, void* k_out,
+                    void* v_out, void* stream) {
+    kvc_status s = check_host_lens(c);
+    if (s) return s;
+    s = check_layer(c, layer);
+    if (s) return s;
+    if (T < 0) return fail(KVC_ERR_ARG, "T = %d < 0", T);
+    if (c->B > 0 && (!first || !count)) return fail(KVC_ERR_ARG, "first / count is null");
+    const int64_t* lens = c->lens.data() + static_cast<size_t>(layer) * c->B;
+    int mx = 0;
+    for (int b = 0; b < c->B; ++b) {
+        if (count[b] < 0 || count[b] > T) return fail(KVC_ERR_SHAPE, "row %d: count = %d outside 0..%d", b, count[b], T);
+        if (count[b] == 0) continue;
+        if (first[b] < 0 || first[b] > lens[b] - count[b])
+            return fail(KVC_ERR_SHAPE, "row %d: positions %lld .. %lld are not all below the row length %lld", b,
+                        static_cast<long long>(first[b]), static_cast<long long>(first[b]) + count[b] - 1,
+                        static_cast<long long>(lens[b]));
+        if (c->ring && first[b] < lens[b] - c->max_len)
+            return fail(KVC_ERR_SHAPE, "row %d: position %lld has left the ring (the oldest stored is %lld)", b,
+                        static_cast<long long>(first[b]), static_cast<long long>(lens[b] - c->max_len));
+        mx = std::max(mx, static_cast<int>(count[b]));
+    }
+    if (mx == 0) return ok();
+    if (!k_out || !v_out) return fail(KVC_ERR_ARG, "k_out / v_out is null");
+    if (!aligned16(k_out) || !aligned16(v_out)) return fail(KVC_ERR_ARG, "k_out / v_out not 16-byte aligned");
+    s = ensure_device(c);
+    if (s) return s;
+    static_assert(sizeof(ReadParams) < 32000, "kernel parameter block too large");
+    ReadParams p;
+    p.k_cache = static_cast<const uint8_t*>(c->k[layer]);
+    p.v_cache = static_cast<const uint8_t*>(c->v[layer]);
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.kind = c->dtype == KVC_Q4 ? kReadQ4 : c->dtype == KVC_FP8_E4M3 ? kReadFp8 : c->dtype == KVC_BF16 ? kReadBf16 : kReadF32;
+    p.B = c->B;
+    p.Hkv = c->Hkv;
+    p.T = T;
+    p.max_len = c->max_len;
+    p.d = c->d;
+    p.ring = c->ring ? 1 : 0;
+    p.pg = c->pg;
+    p.q4 = q4_scales(c, layer);
+    for (int h = 0; h < c->Hkv && p.kind == kReadFp8; ++h) {
+        p.kscale[h] = c->kscale[static_cast<size_t>(layer) * c->Hkv + h];
+        p.vscale[h] = c->vscale[static_cast<size_t>(layer) * c->Hkv + h];
+    }
+    for (int b = 0; b < c->B; ++b) {
+        p.first[b] = count[b] > 0 ? static_cast<int>(first[b]) : 0;
+        p.count[b] = count[b];
+    }
+    cudaError_t e = launch_read_rows(p, mx, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_read launch");
+    ++c->launches;
     return ok();
 }
 
@@ -1351,8 +1482,9 @@ kvc_status kvc_set_window(kvc_cache* c, int window, int ring) {
         if (c->pg.table) return fail(KVC_ERR_ARG, "a paged cache cannot also be a ring");
         if (window < 1 || window > c->max_len) return fail(KVC_ERR_ARG, "a ring cache needs a window of 1..max_len");
         // the largest key tile any kernel of this cache reads
-        const int tile = tc_capable(c) ? 128 : key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
-        if (!generic_path(c) && c->max_len % tile != 0)
+        const bool q4_tiles = c->dtype == KVC_Q4 && (c->d == kHeadDimBf16 || c->d == kHeadDimSmall);
+        const int tile = tc_capable(c) || q4_tiles ? 128 : key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
+        if ((q4_tiles || !generic_path(c)) && c->max_len % tile != 0)
             return fail(KVC_ERR_ARG, "this ring cache needs max_len %% %d == 0 (key tiles never wrap)", tile);
     }
     if ((ring != 0) != c->ring)

@@ -34,6 +34,13 @@ __host__ __device__ __forceinline__ int phys_row(const Paging& pg, int ring, int
     return (b * Hkv + kvh) * max_len + (ring ? a % max_len : a);
 }
 
+// Scale words of a 4-bit cache (one per row, see q4.cuh): a unit's `tokens`
+// words (a KV head's max_len, or a page's) at a stride of `stride` words.
+struct Q4Scales {
+    uint32_t *k, *v;
+    int tokens, stride;
+};
+
 // Keys per K/V tile of the split-KV kernel for 128-wide heads (see
 // key_tile_keys), and the head width the TMA / tensor-core kernels are built
 // for (the split-KV kernel also takes bf16 storage of head width kHeadDimSmall).
@@ -66,11 +73,36 @@ struct AppendParams {
     int fp8;
     float kscale[kMaxScaleHeads];
     float vscale[kMaxScaleHeads];
+    Q4Scales q4;  // 4-bit cache: rows of k_new / v_new are bf16, codes and scale words are stored
     int lens[kMaxBatch];
     int n_new[kMaxBatch];
 };
 
 cudaError_t launch_append(const AppendParams& p, int max_n_new, cudaStream_t stream);
+cudaError_t launch_append_q4(const AppendParams& p, int max_n_new, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Reading rows back: positions first[b] .. first[b] + count[b] - 1 of row b ->
+// k_out / v_out [B, Hkv, T, d] (fp32 of an fp32 cache, else bf16).
+// ---------------------------------------------------------------------------
+enum ReadKind : int { kReadF32 = 0, kReadBf16 = 1, kReadFp8 = 2, kReadQ4 = 3 };
+struct ReadParams {
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    void* k_out;
+    void* v_out;
+    int kind;
+    int B, Hkv, T, max_len, d;
+    int ring;
+    Paging pg;
+    float kscale[kMaxScaleHeads];  // FP8
+    float vscale[kMaxScaleHeads];
+    Q4Scales q4;
+    int first[kMaxBatch];
+    int count[kMaxBatch];
+};
+
+cudaError_t launch_read_rows(const ReadParams& p, int max_count, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Split-KV attention (bf16 storage, fp32 accumulation).
@@ -194,7 +226,8 @@ cudaError_t launch_decode_bf16(const DecodeParams& p, const CUtensorMap& tmK, co
 struct F32Params {
     // kind 0: fp32 storage, queries and outputs; 1: bf16 throughout; 2: FP8
     // E4M3 codes (value = code * kscale / vscale of the KV head), bf16
-    // queries and outputs.
+    // queries and outputs; 3: 4-bit rows (scale words in q4), bf16 queries and
+    // outputs.
     const void* q;
     const void* k_cache;
     const void* v_cache;
@@ -202,6 +235,7 @@ struct F32Params {
     int kind;
     float kscale[kMaxScaleHeads];
     float vscale[kMaxScaleHeads];
+    Q4Scales q4;
     int B, Hq, Hkv, G, T, max_len, d;
     int R;
     int window, ring;  // sliding window (0 = none) and ring storage, as in DecodeParams

@@ -78,7 +78,12 @@ extern "C" {
  * scale per head and dequantize on read).  Their MMAs run in f16 (E4M3 and
  * bf16 convert to f16 exactly within f16's range), so an FP8 cache needs
  * |q| < 65504. */
-typedef enum { KVC_F32 = 0, KVC_BF16 = 1, KVC_FP8_E4M3 = 2 } kvc_dtype;
+typedef enum {
+    KVC_F32 = 0,
+    KVC_BF16 = 1,
+    KVC_FP8_E4M3 = 2,
+    KVC_Q4 = 3 /* 4-bit codes, one step and zero point a row (kvc_create_quantized) */
+} kvc_dtype;
 
 typedef enum {
     KVC_OK = 0,
@@ -146,6 +151,49 @@ kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads
                             int max_pages_per_row, int head_dim, kvc_dtype dtype, void* const* k_bufs,
                             void* const* v_bufs, const int32_t* block_table);
 
+/* A cache held in 4 bits (KVC_Q4).  The pages stop at FP8 (exercise 4); this is
+ * the same idea with half its bytes, and a scale a row in place of one a head.
+ *
+ * A row is one token of one KV head, K and V apart.  It is stored as d codes
+ * of 4 bits, a step s and a zero point z, and stands for the values
+ * s * (c - z).  An appended row x (bf16) gets, every operation rounded to
+ * float32:
+ *   lo = min(0, min x), hi = max(0, max x)
+ *   s  = (hi - lo) / 15, then rounded to bfloat16
+ *   z  = rint(-lo * (1 / s))                      (0 .. 15; ties to even)
+ *   c  = min(15, max(0, rint(x * (1 / s)) + z))   (ties to even)
+ * so that 0 is stored exactly and a value is off by at most half a step (0.56
+ * of one at the row's upper end, where s was rounded down).  A row whose s is below 2^-126 is stored as zeros (s, z and codes
+ * 0).  A row that holds a NaN or an infinity, or whose range passes float32,
+ * has s = NaN and reads as NaN in every place, in attention too.
+ *
+ * Buffers.  k_bufs[l] / v_bufs[l]: [B, Hkv, max_len, d / 2] bytes; eight
+ * consecutive values of a row share a little-endian 32-bit word, value 2i at
+ * bits 4i and value 2i + 1 at bits 16 + 4i.  k_scales[l] / v_scales[l]:
+ * 32-bit words [B, Hkv, S], S = max_len rounded up to a multiple of 4; word
+ * [b][h][a] has s (bfloat16) in its high 16 bits and z in its low 16.  Other
+ * producers may fill them (kvc_set_lens); codes need no check, a z above 15
+ * counts as it stands.  head_dim is a multiple of 32, at most 256; all buffers
+ * are 16-byte aligned.  q, k_new, v_new and out are bf16.
+ *
+ * Every call of this header serves such a cache as it serves an FP8 one, with
+ * these limits: kvc_set_kv_scales does not apply; pages and rings of head_dim
+ * 64 and 128 hold a multiple of 128 tokens.
+ * Errors: as kvc_create and kvc_create_paged, and KVC_ERR_ARG for null or
+ * misaligned scale buffers. */
+kvc_status kvc_create_quantized(kvc_cache** out, int layers, int batch, int kv_heads, int max_len, int head_dim,
+                                void* const* k_bufs, void* const* v_bufs, void* const* k_scales,
+                                void* const* v_scales);
+
+/* The same behind a block table (see kvc_create_paged): k_bufs[l] / v_bufs[l]
+ * are [num_pages, kv_heads, page_size, head_dim / 2] bytes, k_scales[l] /
+ * v_scales[l] 32-bit words [num_pages, kv_heads, S], S = page_size rounded up
+ * to a multiple of 4. */
+kvc_status kvc_create_quantized_paged(kvc_cache** out, int layers, int batch, int kv_heads, int page_size,
+                                      int num_pages, int max_pages_per_row, int head_dim, void* const* k_bufs,
+                                      void* const* v_bufs, void* const* k_scales, void* const* v_scales,
+                                      const int32_t* block_table);
+
 /* Append in place ("A strong answer", KVCache.append): for every row b and
  * t < n_new[b], copy k_new[b, :, t, :] to K[b, :, lens[b] + t, :] (same for
  * V), then lens[layer][b] += n_new[b].  n_new is a HOST array of B entries.
@@ -155,6 +203,22 @@ kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads
  * (lens[b] + n_new[b] > max_len for any row), KVC_ERR_CUDA (launch failed). */
 kvc_status kvc_append(kvc_cache* c, int layer, const void* k_new, const void* v_new, int T,
                       const int32_t* n_new, void* stream);
+
+/* Read rows back: positions first[b] .. first[b] + count[b] - 1 of row b go to
+ * k_out[b, :, 0 .. count[b] - 1, :] and v_out likewise, both [B, Hkv, T, d]
+ * in the type of q (fp32 of an fp32 cache, else bf16): a copy of an fp32 or
+ * bf16 cache, the E4M3 code times its head's scale of an FP8 one, s * (c - z)
+ * of a 4-bit one, each rounded once to bf16.  first (int64) and count (int32)
+ * are HOST arrays of B entries.  Entries t >= count[b] of the outputs are left
+ * as they were; first[b] is not looked at where count[b] is 0.  In a ring
+ * cache the positions must still be stored (the last max_len of the row).  A
+ * position whose block-table entry is outside 0 .. num_pages - 1 reads as
+ * zeros.  No workspace.
+ * Errors (outputs untouched): KVC_ERR_ARG (layer, pointers, alignment, T < 0,
+ * lengths on the device), KVC_ERR_SHAPE (count[b] outside 0..T, positions that
+ * the row does not hold), KVC_ERR_CUDA. */
+kvc_status kvc_read(kvc_cache* c, int layer, const int64_t* first, const int32_t* count, int T, void* k_out,
+                    void* v_out, void* stream);
 
 /* Bytes of device workspace kvc_gqa_attention needs for this handle, q_heads
  * and T (an error word and the split-KV partial results).

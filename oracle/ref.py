@@ -255,6 +255,75 @@ def e4m3_dequantize(codes, scale: float) -> np.ndarray:
     return lut[codes] * float(scale)
 
 
+# ---------------------------------------------------------------------------
+# 4-bit rows: one step and zero point a row, written out from the format's
+# definition (lo = min(0, min x), hi = max(0, max x), s = bf16((hi - lo) / 15),
+# z = rint(-lo / s), c = clamp(rint(x / s) + z, 0, 15), value = s (c - z), with
+# 1/s and each product rounded to float32).
+# ---------------------------------------------------------------------------
+
+
+def bf16_round(x) -> np.ndarray:
+    """Nearest bfloat16 (ties to even) of float32 values, as float64."""
+    x = np.asarray(x, dtype=np.float32)
+    u = x.view(np.uint32).astype(np.uint64)
+    r = ((u + 0x7FFF + ((u >> 16) & 1)) & 0xFFFF0000).astype(np.uint32)
+    y = r.view(np.float32).astype(np.float64)
+    return np.where(np.isnan(x), np.nan, y)
+
+
+def _f32(x) -> np.ndarray:
+    """Round float64 to float32, kept as float64."""
+    with np.errstate(over="ignore"):
+        return np.asarray(x, dtype=np.float64).astype(np.float32).astype(np.float64)
+
+
+def q4_quantize(x):
+    """(codes [..., d], step [...], zero point [...]) of bf16 rows x [..., d]."""
+    x = np.asarray(x, dtype=np.float64)
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        lo = np.minimum(0.0, np.min(x, axis=-1))
+        hi = np.maximum(0.0, np.max(x, axis=-1))
+        span = _f32(hi - lo)
+        s = bf16_round(_f32(span / 15.0))
+        r = _f32(1.0 / s)
+        z = np.rint(_f32(-lo * r))
+        c = np.clip(np.rint(_f32(x * r[..., None])) + z[..., None], 0, 15)
+    tiny = np.isfinite(span) & (s < 2.0 ** -126)
+    bad = ~np.isfinite(span)
+    s = np.where(tiny, 0.0, np.where(bad, np.nan, s))
+    z = np.where(tiny | bad, 0.0, z)
+    c = np.where((tiny | bad)[..., None], 0.0, c)
+    return c.astype(np.int64), s, z.astype(np.int64)
+
+
+def q4_values(codes, s, z) -> np.ndarray:
+    """s * (c - z), exactly (float64)."""
+    return np.asarray(s, dtype=np.float64)[..., None] * (np.asarray(codes) - np.asarray(z)[..., None])
+
+
+def q4_store(x) -> np.ndarray:
+    """The values that rows x [..., d] stand for once they are stored in 4 bits."""
+    return q4_values(*q4_quantize(x))
+
+
+def q4_pack(codes) -> np.ndarray:
+    """Code words (uint32 [..., d / 8]): value 2i of a word at bits 4i, value 2i + 1 at bits 16 + 4i."""
+    c = np.asarray(codes, dtype=np.uint32)
+    c = c.reshape(*c.shape[:-1], -1, 8)
+    w = np.zeros(c.shape[:-1], dtype=np.uint32)
+    for i in range(4):
+        w |= c[..., 2 * i] << np.uint32(4 * i)
+        w |= c[..., 2 * i + 1] << np.uint32(16 + 4 * i)
+    return w
+
+
+def q4_scale_words(s, z) -> np.ndarray:
+    """Scale words (uint32): the step as bfloat16 in the high half, the zero point in the low half."""
+    bits = np.asarray(s, dtype=np.float64).astype(np.float32).view(np.uint32) & np.uint32(0xFFFF0000)
+    return bits | np.asarray(z).astype(np.uint32)
+
+
 class OracleCache:
     """Preallocated KV cache with per-layer, per-row valid lengths.
 

@@ -1,0 +1,420 @@
+"""The 4-bit cache on the GPU against the float64 oracle.
+
+Stored codes and scale words must equal the oracle's bit for bit on every
+path that writes them, rows read back must be the oracle's values rounded once
+to bf16, and attention must stay within a bound worked out from the roundings
+its kernels make (``_bound``).  Slots never written hold 0xFF bytes: code 15
+and a NaN step, so a read of one shows.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.ref as ref
+from gqa_attention_preallocated_gb300 import KVCache, KVCError, PagedKVCache
+from gqa_attention_preallocated_gb300 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+U16, UB = 2.0 ** -11, 2.0 ** -8  # half a unit in the last place of f16, of bf16
+
+
+@pytest.fixture(autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+
+
+def _bf(x):
+    return wl.to_storage(x, torch.bfloat16)
+
+
+def _attend(q, K, V, lens, n_new, window=0, parents=None):
+    """(out, sum p |v| / sum p, largest sum |q k| / sqrt d over a query's keys) in float64.
+
+    q [B, Hq, T, d]; K, V: per row [Hkv, len, d], row b's tokens at their positions."""
+    B, Hq, T, d = q.shape
+    out, mass = np.zeros(q.shape), np.zeros(q.shape)
+    dot = np.zeros((B, Hq, T, 1))
+    for b in range(B):
+        n, L = int(n_new[b]), int(lens[b])
+        if n == 0:
+            continue
+        Hkv = K[b].shape[0]
+        G = Hq // Hkv
+        pos = L - n + np.arange(n)
+        key = np.arange(L)
+        see = key[None, :] <= pos[:, None]
+        if window:
+            see &= key[None, :] > pos[:, None] - window
+        if parents is not None:
+            for t in range(n):
+                see[t, L - n:] = False
+                for u in ref.tree_path(parents[b], t):
+                    see[t, L - n + u] = True
+        for h in range(Hkv):
+            x = np.einsum("gtd,sd->gts", q[b, h * G:(h + 1) * G, :n], K[b][h]) / math.sqrt(d)
+            x = np.where(see[None], x, -np.inf)
+            p = np.exp(x - x.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            Vh = np.where(see.any(0)[:, None], V[b][h], 0.0)
+            out[b, h * G:(h + 1) * G, :n] = p @ Vh
+            mass[b, h * G:(h + 1) * G, :n] = p @ np.abs(Vh)
+            a = np.einsum("gtd,sd->gts", np.abs(q[b, h * G:(h + 1) * G, :n]), np.abs(K[b][h])) / math.sqrt(d)
+            dot[b, h * G:(h + 1) * G, :n, 0] = np.where(see[None], a, 0.0).max(-1)
+    return out, mass, dot
+
+
+def _bound(want, mass, dot, rows):
+    """Largest |got - want| that the kernels' roundings allow.
+
+    The output is rounded to bf16.  Up to 16 query rows per KV head the codes
+    and queries enter the products exactly and only the softmax weights are
+    rounded, to f16.  Above, the rows are rounded to bf16 on their way to the
+    tensor core (K: each score moves by at most UB * sum |q k| / sqrt d, so each
+    weight by twice that; V: by UB) and the weights too.  float32 sums, exp2
+    and the norm add 2^-16 of the mass, and 2^-20 * sum |q k| / sqrt d in the
+    scores."""
+    up, uv, uk = (U16, 0.0, 0.0) if rows <= 16 else (UB, UB, UB)
+    shift = 2 * np.expm1((uk + 2.0 ** -20) * dot)
+    return UB * np.abs(want) + mass * (1 + UB) * (up + uv + shift + 2.0 ** -16) + 1e-30
+
+
+class Pair:
+    """A 4-bit cache and the rows the oracle says it holds (per row b: [Hkv, len, d] values)."""
+
+    def __init__(self, B, Hkv, d, max_len, window=0, ring=False, page=0, layers=1, layer=0, seed=0):
+        self.B, self.Hkv, self.d, self.max_len, self.window, self.ring, self.page = B, Hkv, d, max_len, window, ring, page
+        self.layer, self.rng, self.seed = layer, np.random.default_rng(seed + 1000), seed
+        if page:
+            mpr = max_len // page
+            num = B * mpr + 3
+            self.c = PagedKVCache(layers, B, Hkv, page, num, mpr, d, dtype="q4")
+            self.table = self.rng.permutation(num)[: B * mpr].reshape(B, mpr)
+            self.c.block_table.copy_(torch.as_tensor(self.table, dtype=torch.int32))
+        else:
+            self.c = KVCache(layers, B, Hkv, max_len, d, dtype="q4")
+        for bufs in (self.c.k, self.c.v, self.c.k_scale, self.c.v_scale):
+            for t in bufs:
+                t.view(torch.uint8).fill_(0xFF)
+        if window:
+            self.c.set_window(window, ring=ring)
+        self.x = [[np.zeros((Hkv, 0, d)) for _ in range(B)] for _ in range(2)]  # appended bf16 rows, K and V
+        self.calls = 0
+
+    @property
+    def lens(self):
+        return np.array([r.shape[1] for r in self.x[0]])
+
+    def inputs(self, n_new, T, G, scale=1.0, spread=0.0):
+        self.calls += 1
+        s = self.seed * 100 + self.calls
+        mk = lambda i, H: wl.normal(s, i, (self.B, H, T, self.d))  # noqa: E731
+        bias = spread * wl.normal(s, 9, (1, 1, 1, self.d))
+        return _bf(mk(1, self.Hkv * G)), _bf(mk(2, self.Hkv) * scale + bias), _bf(mk(3, self.Hkv) * scale)
+
+    def note(self, k, v, n_new):
+        for x, new in ((self.x[0], k), (self.x[1], v)):
+            new = new.double().numpy()
+            for b in range(self.B):
+                x[b] = np.concatenate([x[b], new[b, :, : int(n_new[b])]], axis=1)
+
+    def values(self):
+        return [[ref.q4_store(r) for r in x] for x in self.x]
+
+    def check_out(self, out, q, n_new, T, parents=None, tag=""):
+        K, V = self.values()
+        want, mass, dot = _attend(q.double().numpy(), K, V, self.lens, n_new, self.window, parents)
+        got = out.double().cpu().numpy()
+        for b in range(self.B):
+            assert np.all(got[b, :, int(n_new[b]):] == 0.0), (tag, b)
+        G = q.shape[1] // self.Hkv
+        lim = _bound(want, mass, dot, G * T)
+        over = np.abs(got - want) - lim
+        assert np.isfinite(got).all(), tag
+        assert over.max() <= 0, (tag, float(over.max()), float(np.abs(got - want).max()))
+        assert self.c.device_status() == 0
+
+    def step(self, n_new, G, T=None, parents=None, split=False, **kw):
+        """One chunk: append_attention (or append, then attention) against the oracle."""
+        n_new = np.asarray(n_new)
+        T = max(1, int(n_new.max())) if T is None else T
+        q, k, v = self.inputs(n_new, T, G, **kw)
+        if parents is not None:
+            out = self.c.append_attention_tree(self.layer, q.cuda(), k.cuda(), v.cuda(), n_new, parents)
+        elif split:
+            self.c.append(self.layer, k.cuda(), v.cuda(), n_new)
+            out = self.c.gqa_attention(self.layer, q.cuda(), n_new)
+        else:
+            out = self.c.append_attention(self.layer, q.cuda(), k.cuda(), v.cuda(), n_new)
+        self.note(k, v, n_new)
+        assert np.array_equal(self.c.lens(self.layer), self.lens)
+        self.check_out(out, q, n_new, T, parents, tag=(self.calls, T, G))
+        return out
+
+    def check_store(self):
+        """Codes and scale words of every stored position, bit for bit, and the rows read back."""
+        kc, vc = (t[self.layer].cpu().numpy() for t in (self.c.k, self.c.v))
+        ks, vs = (t[self.layer].cpu().numpy().view(np.uint32) for t in (self.c.k_scale, self.c.v_scale))
+        lens = self.lens
+        for codes, words, x in ((kc, ks, self.x[0]), (vc, vs, self.x[1])):
+            used = np.zeros(words.shape, dtype=bool)
+            for b in range(self.B):
+                c, s, z = ref.q4_quantize(x[b])
+                for a in range(max(0, lens[b] - self.max_len) if self.ring else 0, lens[b]):
+                    e, at = (self.table[b, a // self.page], a % self.page) if self.page else (b, a % self.max_len)
+                    assert np.array_equal(codes[e, :, at].view(np.uint32), ref.q4_pack(c[:, a])), (b, a)
+                    assert np.array_equal(words[e, :, at], ref.q4_scale_words(s[:, a], z[:, a])), (b, a)
+                    used[e, :, at] = True
+            assert np.all(words[~used] == 0xFFFFFFFF) and np.all(codes[~used[..., : codes.shape[2]]] == 0xFF)
+        first = np.maximum(0, lens - self.max_len) if self.ring else np.zeros(self.B, dtype=np.int64)
+        K, V = self.c.read(self.layer, first, lens - first)
+        for got, x in ((K, self.x[0]), (V, self.x[1])):
+            got = got.double().cpu().numpy()
+            for b in range(self.B):
+                want = ref.bf16_round(ref.q4_store(x[b][:, first[b]:]).astype(np.float32))
+                assert np.array_equal(got[b, :, : lens[b] - first[b]], want)
+                assert not got[b, :, lens[b] - first[b]:].any()
+
+
+# ------------------------------------------------------------------ storing
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 160, 256])
+def test_append_and_read(d):
+    p = Pair(3, 2, d, 67, seed=d)  # an odd length: the scale words' stride is not max_len
+    for n in ([1, 0, 1], [17, 64, 3], [0, 3, 40]):
+        T = max(n) + 2
+        q, k, v = p.inputs(n, T, 1, scale=2.5, spread=3.0)
+        p.c.append(0, k.cuda(), v.cuda(), np.array(n))
+        p.note(k, v, n)
+    p.check_store()
+
+
+def test_append_special_rows():
+    """Rows of zeros, of one sign, of one value, tiny, huge, with NaN and infinities."""
+    d, T = 128, 12
+    x = wl.normal(5, 1, (1, 1, T, d)).float()
+    x[0, 0, 0] = 0
+    x[0, 0, 1] = x[0, 0, 1].abs() + 3
+    x[0, 0, 2] = -x[0, 0, 2].abs() - 3
+    x[0, 0, 3] = 0.75
+    x[0, 0, 4] *= 2.0 ** -128
+    x[0, 0, 5] *= 2.0 ** -122
+    x[0, 0, 6] *= 2.0 ** 120
+    x[0, 0, 7, 5] = math.nan
+    x[0, 0, 8, 127] = math.inf
+    x[0, 0, 9, 0] = -math.inf
+    x[0, 0, 10, :2] = torch.tensor([3e38, -3e38])
+    x = x.to(torch.bfloat16)
+    c = KVCache(1, 1, 1, 16, d, dtype="q4")
+    c.append(0, x.cuda(), x.flip(3).contiguous().cuda(), [T])
+    codes, s, z = ref.q4_quantize(x.double().numpy()[0, 0])
+    assert np.array_equal(c.k[0].cpu().numpy()[0, 0, :T].view(np.uint32), ref.q4_pack(codes))
+    assert np.array_equal(c.k_scale[0].cpu().numpy().view(np.uint32)[0, 0, :T], ref.q4_scale_words(s, z))
+    k, v = c.read(0, [0], [T])
+    got, want = k.double().cpu().numpy()[0, 0], ref.q4_values(codes, s, z)
+    want = ref.bf16_round(want.astype(np.float32))
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~np.isnan(got)], want[~np.isnan(want)])
+    assert np.isnan(got[7:11]).all() and np.isfinite(got[[0, 1, 2, 3, 4, 5, 6, 11]]).all()
+    assert torch.equal(torch.nan_to_num(v.flip(3), nan=9.0), torch.nan_to_num(k, nan=9.0))
+
+
+def test_codes_at_ties():
+    """Values on the borders between codes round to the even code, as the definition says."""
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    x[0, 0, 0, :16] = torch.arange(16).to(torch.bfloat16) - 7       # range 15: step 1
+    x[0, 0, 0, 16:31] = torch.arange(15).to(torch.bfloat16) - 6.5   # every border
+    p = KVCache(1, 1, 1, 8, 64, dtype="q4")
+    p.append(0, x.cuda(), x.cuda(), [1])
+    k, _ = p.read(0, [0], [1])
+    want = torch.arange(16).float() - 7
+    assert torch.equal(k[0, 0, 0, :16].float().cpu(), want)
+    assert torch.equal(k[0, 0, 0, 16:31].float().cpu(), torch.round(torch.arange(15).float() - 6.5))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("page", [0, 128])
+def test_read_of_the_other_types(dtype, page):
+    B, Hkv, d, L = 2, 2, 64 if dtype != torch.float8_e4m3fn else 128, 256
+    io = torch.float32 if dtype == torch.float32 else torch.bfloat16
+    if page:
+        c = PagedKVCache(1, B, Hkv, page, 5, 2, d, dtype=dtype)
+        c.block_table.copy_(torch.tensor([[4, 0], [2, 1]], dtype=torch.int32))
+    else:
+        c = KVCache(1, B, Hkv, L, d, dtype=dtype)
+    ks, vs = np.array([0.01, 0.02], np.float32), np.array([0.5, 0.25], np.float32)
+    if dtype == torch.float8_e4m3fn:
+        c.set_kv_scales(0, ks, vs)
+    k, v = (wl.to_storage(wl.normal(8, i, (B, Hkv, 200, d)), io) for i in (1, 2))
+    c.append(0, k.cuda(), v.cuda(), [200, 131])
+    out = [torch.full((B, Hkv, 77, d), 5.0, dtype=io, device="cuda") for _ in range(2)]
+    c.read(0, [100, 60], [77, 71], k_out=out[0], v_out=out[1])
+    for got, x, s in ((out[0], k, ks), (out[1], v, vs)):
+        got = got.cpu()
+        for b, (f, n) in enumerate(((100, 77), (60, 71))):
+            want = x[b, :, f:f + n]
+            if dtype == torch.float8_e4m3fn:
+                want = np.stack([ref.e4m3_dequantize(ref.e4m3_quantize(want[h].double().numpy(), s[h]), s[h]) for h in range(Hkv)])
+                want = torch.from_numpy(ref.bf16_round(want.astype(np.float32))).to(io)
+            assert torch.equal(got[b, :, :n], want)
+            assert torch.all(got[b, :, n:] == 5.0)
+
+
+def test_read_through_a_bad_page_is_zeros():
+    c = PagedKVCache(1, 1, 1, 128, 2, 2, 128, dtype="q4")
+    x = torch.ones(1, 1, 256, 128, dtype=torch.bfloat16, device="cuda")
+    c.append(0, x, x, [256])
+    c.block_table[0, 1] = 2  # outside 0 .. num_pages - 1
+    k, v = c.read(0, [0], [256])
+    assert torch.all(k[0, 0, :128] == 1.0) and torch.all(k[0, 0, 128:] == 0.0) and torch.equal(k, v)
+
+
+# ---------------------------------------------------------------- attention
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 256])
+@pytest.mark.parametrize("G,chunks", [
+    (1, [[1, 1, 0], [1, 1, 1], [1, 0, 1]]),              # from empty rows on, single tokens
+    (4, [[63, 1, 130], [1, 1, 1], [1, 0, 1], [1, 1, 1]]),  # decode around a tile's end
+    (3, [[70, 128, 5], [4, 5, 1], [5, 5, 5]]),           # short verify: 12 to 15 rows per KV head
+    (8, [[129, 64, 0], [2, 1, 2], [3, 4, 4]]),           # 16 to 32 rows
+    (7, [[40, 90, 77], [9, 9, 8]]),                      # 63 rows
+])
+def test_chunks(d, G, chunks):
+    p = Pair(3, 2, d, 203, seed=d + G)
+    for i, n in enumerate(chunks):
+        p.step(n, G, T=max(n) + (1 if i == 1 else 0), spread=1.0 if i == 0 else 0.0)
+    p.check_store()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 5])
+def test_prefill(d, G):
+    p = Pair(2, 2, d, 700, seed=G)
+    p.step([300, 129], G, spread=1.0)
+    p.step([150, 200], G)
+    p.step([0, 33], G, split=True)
+    p.step([1, 1], G)
+    p.check_store()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages(d):
+    p = Pair(3, 2, d, 512, page=128, seed=4)
+    for n, G in (([130, 0, 257], 4), ([1, 1, 1], 4), ([126, 5, 0], 4), ([4, 3, 4], 4), ([1, 1, 1], 8)):
+        p.step(n, G)
+    p.check_store()
+
+
+def test_pages_of_odd_size():
+    p = Pair(2, 2, 96, 90, page=18, seed=6)
+    for n in ([19, 35], [1, 1], [5, 2], [17, 18]):
+        p.step(n, 4)
+    p.check_store()
+
+
+@pytest.mark.parametrize("d,page", [(64, 0), (128, 0), (128, 128), (96, 0)])
+@pytest.mark.parametrize("window", [1, 7, 64, 150])
+def test_window(d, page, window):
+    p = Pair(2, 2, d, 512, window=window, page=page, seed=window)
+    for n in ([200, 3], [1, 1], [140, 129], [5, 4], [1, 0], [1, 1]):
+        p.step(n, 4)
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+def test_ring(d):
+    p = Pair(2, 2, d, 256, window=100, ring=True, seed=d)
+    for n in ([150, 157], [100, 1], [1, 1], [4, 3], [120, 157], [1, 1], [1, 0], [150, 60], [1, 1]):
+        p.step(n, 4)
+    p.check_store()
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("G,T", [(1, 6), (4, 4), (4, 7), (8, 8)])
+def test_trees(d, G, T):
+    rng = np.random.default_rng(G * T)
+    p = Pair(3, 2, d, 300, seed=T)
+    p.step([100, 0, 64], G)
+    for n in ([T, T, T - 1], [T, 1, T]):
+        parents = np.array([[rng.integers(-1, t) if t else -1 for t in range(T)] for _ in range(3)])
+        p.step(n, G, T=T, parents=parents)
+    p.check_store()
+
+
+def test_scales_of_very_different_size():
+    """Rows whose steps span 2^40, and queries of very different size, neither overflow nor vanish."""
+    p = Pair(2, 1, 128, 300, seed=3)
+    n = 120
+    f = torch.tensor(2.0) ** torch.linspace(-20, 20, n)[None, None, :, None]
+    q, k, v = p.inputs([n, n], n, 4)
+    k = _bf(k.double() * 2.0 ** -3)
+    v = _bf(v.double() * f.double())
+    p.c.append(0, k.cuda(), v.cuda(), [n, n])
+    p.note(k, v, [n, n])
+    for T, scale in ((1, 1.0), (1, 2.0 ** -60), (1, 2.0 ** 4), (3, 1.0), (40, 1.0)):
+        q, _, _ = p.inputs([T, T], T, 4)
+        q = _bf(q.double() * scale)
+        out = p.c.gqa_attention(0, q.cuda(), [T, T])
+        p.check_out(out, q, [T, T], T, tag=(T, scale))
+
+
+def test_nan_rows_reach_their_queries_only():
+    """A NaN row shows in the queries that see it and nowhere else (window, tree and causal masks)."""
+    for d in (64, 96, 128):
+        p = Pair(1, 1, d, 256, window=8, seed=d)
+        q, k, v = p.inputs([40], 40, 2)
+        v = v.clone()
+        v[0, 0, 10, 3] = math.nan
+        out = p.c.append_attention(0, q.cuda(), k.cuda(), v.cuda(), [40]).float().cpu()
+        bad = torch.isnan(out).any(-1)[0]
+        assert bad[:, 10:18].all() and not bad[:, :10].any() and not bad[:, 18:].any()
+        # decode: the row has left the window
+        q, k, v = p.inputs([1], 1, 2)
+        assert torch.isfinite(p.c.append_attention(0, q.cuda(), k.cuda(), v.cuda(), [1])).all()
+        t = Pair(1, 1, d, 64, seed=d)
+        t.step([20], 2)
+        q, k, v = t.inputs([3], 3, 2)
+        k, v = k.clone(), v.clone()
+        k[0, 0, 1, 0], v[0, 0, 1, 5] = math.inf, math.nan
+        out = t.c.append_attention_tree(0, q.cuda(), k.cuda(), v.cuda(), [3], [[-1, 0, 0]]).float().cpu()
+        bad = torch.isnan(out).any(-1)[0]
+        assert bad[:, 1].all() and not bad[:, 0].any() and not bad[:, 2].any()
+
+
+def test_layers_truncate_and_host_buffers():
+    p = Pair(2, 2, 128, 256, layers=2, layer=1, seed=2)
+    p.step([70, 33], 4)
+    p.c.append(0, *(t.cuda() for t in p.inputs([70, 33], 70, 4)[1:]), [70, 33])
+    p.c.truncate([50, 33])
+    for x in p.x:
+        x[0] = x[0][:, :50]
+    p.step([1, 1], 4)
+    q, k, v = (t.pin_memory() for t in p.inputs([2, 1], 3, 4))
+    out = torch.zeros(q.shape, dtype=torch.bfloat16).pin_memory()
+    p.c.append_attention_host(1, q, k, v, [2, 1], out)
+    p.c.host_copies_done()
+    torch.cuda.synchronize()
+    p.note(k, v, [2, 1])
+    p.check_out(out, q, [2, 1], 3)
+
+
+def test_refusals():
+    c = KVCache(1, 1, 1, 64, 128, dtype="q4")
+    q = torch.zeros(1, 2, 1, 128, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (q.float(), q[..., :64], q.transpose(1, 2)):
+        with pytest.raises(KVCError):
+            c.append_attention(0, bad, kv, kv, [1])
+    with pytest.raises(KVCError):
+        c.set_kv_scales(0, [1.0], [1.0])
+    with pytest.raises(KVCError):
+        KVCache(1, 1, 1, 64, 128, dtype=torch.bfloat16, k_scales=[q])
+    with pytest.raises(KVCError):
+        KVCache(1, 1, 1, 64, 128, dtype="q4", k_bufs=[torch.zeros(1, 1, 64, 128, dtype=torch.uint8, device="cuda")])
+    with pytest.raises(KVCError):
+        c.read(0, [0], [1])
+    with pytest.raises(KVCError):
+        c.read(0, [0], [0], k_out=kv)
+    with pytest.raises(KVCError):
+        c.append(0, kv.expand(1, 1, 65, 128).contiguous(), kv.expand(1, 1, 65, 128).contiguous(), [65])
+    assert c.lens(0)[0] == 0
