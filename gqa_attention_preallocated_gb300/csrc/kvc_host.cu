@@ -89,11 +89,15 @@ int tc_min_rows(const kvc_cache* c) { return c->dtype == KVC_FP8_E4M3 ? kTcMinRo
 // bf16 or FP8 storage whose head dimension has no TMA kernel (the split-KV
 // kernel takes d = 128, and d = 64 for bf16; the tensor-core kernel d = 128).
 bool generic_path(const kvc_cache* c) {
-    return c->dtype == KVC_F32 || c->dtype == KVC_Q4 ||
-           !(c->d == kHeadDimBf16 || (c->d == kHeadDimSmall && c->dtype == KVC_BF16));
+    return c->dtype == KVC_F32 ||
+           !(c->d == kHeadDimBf16 || (c->d == kHeadDimSmall && (c->dtype == KVC_BF16 || c->dtype == KVC_Q4)));
 }
 // Head dimension the tensor-core kernel is built for.
-bool tc_capable(const kvc_cache* c) { return !generic_path(c) && c->d == kHeadDimBf16; }
+bool tc_capable(const kvc_cache* c) { return !generic_path(c) && c->d == kHeadDimBf16 && c->dtype != KVC_Q4; }
+// Keys per tile of the split-KV kernel that serves this cache.
+int split_tile_keys(const kvc_cache* c) {
+    return c->dtype == KVC_Q4 ? kQ4KeyTile : key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
+}
 // Calls with more query rows per KV head than the split-KV kernel's 64 on a
 // cache the tensor-core kernel cannot take (bf16, d = 64) run on the generic kernel.
 bool generic_call(const kvc_cache* c, int R) { return generic_path(c) || (!tc_capable(c) && R > 64); }
@@ -181,12 +185,34 @@ kvc_status encode_rows_map(CUtensorMap* m, const void* base, cuuint64_t rows, cu
     return ok();
 }
 
+// The codes of a 4-bit cache: [rows, d / 2 bytes], boxes of 64 rows, with the
+// 64-byte swizzle for 64-byte rows (d = 128).
+kvc_status encode_q4_map(CUtensorMap* m, const void* base, cuuint64_t rows, int d) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(d / 2), rows};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d / 2)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(d / 2), 64};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return ok();
+}
+
 // One layer's K and V as rows = B*Hkv*max_len: 64-row and 128-row boxes.
 kvc_status encode_layer_maps(kvc_cache* c, int layer) {
     if (c->tm_ready[layer]) return ok();
     const cuuint64_t rows = c->pg.table ? static_cast<cuuint64_t>(c->pg.num_pages) * c->Hkv * c->pg.page
                                         : static_cast<cuuint64_t>(c->B) * c->Hkv * c->max_len;
     kvc_status s;
+    if (c->dtype == KVC_Q4) {
+        if ((s = encode_q4_map(&c->tmK[layer], c->k[layer], rows, c->d))) return s;
+        if ((s = encode_q4_map(&c->tmV[layer], c->v[layer], rows, c->d))) return s;
+        c->tm_ready[layer] = 1;
+        return ok();
+    }
     const bool fp8 = c->dtype == KVC_FP8_E4M3;
     const int kt = key_tile_keys(c->d, fp8);  // the split-KV kernel's tile for this cache
     if ((s = encode_rows_map(&c->tmK[layer], c->k[layer], rows, kt, fp8, c->d))) return s;
@@ -270,7 +296,8 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
     pl->generic = generic_call(c, pl->R);
     if (!pl->generic) {
         pl->mt = pl->R <= 16 ? 1 : (pl->R <= 32 ? 2 : 4);
-        pl->RPB = 16 * pl->mt;
+        // 4-bit caches: blocks of 8 or 16 rows (more rows re-read the tiles).
+        pl->RPB = c->dtype == KVC_Q4 ? (pl->R <= 8 ? 8 : 16) : 16 * pl->mt;
         pl->RB = std::max(1, (pl->R + pl->RPB - 1) / pl->RPB);
         // Only the split-KV kernel works in (row, row block) groups.  A call
         // with more than 64 rows per KV head (more than any tree call takes)
@@ -289,7 +316,7 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
         // device-computed plans of resident-length steps, then the ancestor
         // masks of a tree-verify call
         pl->ws_plan = round_up(sizeof(DevicePlan), 256) + round_up(kMaxTreeQueries * sizeof(uint64_t), 256);
-        pl->ways = decode_launch_shape(pl->mt, c->dtype == KVC_FP8_E4M3, c->d).ways;
+        pl->ways = c->dtype == KVC_Q4 ? 1 : decode_launch_shape(pl->mt, c->dtype == KVC_FP8_E4M3, c->d).ways;
         pl->part_rows = std::min(pl->R, pl->RPB);
         pl->ws_partials = tc_only ? 0
                                   : static_cast<size_t>(pl->units + num_ctas) * pl->ways * pl->part_rows *
@@ -674,6 +701,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     p.ring = c->ring ? 1 : 0;
     p.pg = c->pg;
     set_decode_scales(c, layer, &p);
+    p.q4 = q4_scales(c, layer);
     p.anc = nullptr;
     if (anc) {
         // The masks go to the workspace (the parameter block stays small).
@@ -711,7 +739,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 }
             }
             const int kfirst = (extent > 0 && c->window > 0) ? std::max(0, qmin - c->window + 1) : 0;
-            const int kt = key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
+            const int kt = split_tile_keys(c);
             const int first_tile = kfirst / kt;
             const int ntiles = extent > 0 ? (extent - 1) / kt + 1 - first_tile : 0;
             p.gstart[b * pl.RB + rb] = static_cast<int>(tiles);
@@ -759,7 +787,9 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         c->last_ws = ws;
     }
     cudaError_t e =
-        launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], pl.mt, grid, c->dtype == KVC_FP8_E4M3, c->d, stream);
+        c->dtype == KVC_Q4
+            ? launch_decode_q4(p, c->tmK[layer], c->tmV[layer], grid, c->d, stream)
+            : launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], pl.mt, grid, c->dtype == KVC_FP8_E4M3, c->d, stream);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV attention launch");
     ++c->launches;
     if (main_enqueued) *main_enqueued = true;
@@ -1482,9 +1512,8 @@ kvc_status kvc_set_window(kvc_cache* c, int window, int ring) {
         if (c->pg.table) return fail(KVC_ERR_ARG, "a paged cache cannot also be a ring");
         if (window < 1 || window > c->max_len) return fail(KVC_ERR_ARG, "a ring cache needs a window of 1..max_len");
         // the largest key tile any kernel of this cache reads
-        const bool q4_tiles = c->dtype == KVC_Q4 && (c->d == kHeadDimBf16 || c->d == kHeadDimSmall);
-        const int tile = tc_capable(c) || q4_tiles ? 128 : key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
-        if ((q4_tiles || !generic_path(c)) && c->max_len % tile != 0)
+        const int tile = tc_capable(c) ? 128 : split_tile_keys(c);
+        if (!generic_path(c) && c->max_len % tile != 0)
             return fail(KVC_ERR_ARG, "this ring cache needs max_len %% %d == 0 (key tiles never wrap)", tile);
     }
     if ((ring != 0) != c->ring)
@@ -1595,7 +1624,7 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     pp.max_len = c->max_len;
     pp.window = c->window;
     pp.ring = c->ring ? 1 : 0;
-    pp.key_tile = key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
+    pp.key_tile = split_tile_keys(c);
     cudaError_t e = launch_decode_plan(pp, st);
     if (e != cudaSuccess) return cuda_fail(e, "device plan launch");
     ++c->launches;
@@ -1630,7 +1659,9 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     p.ring = c->ring ? 1 : 0;
     p.pg = c->pg;
     set_decode_scales(c, layer, &p);
-    e = launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], 1, grid, c->dtype == KVC_FP8_E4M3, c->d, st);
+    p.q4 = q4_scales(c, layer);
+    e = c->dtype == KVC_Q4 ? launch_decode_q4(p, c->tmK[layer], c->tmV[layer], grid, c->d, st)
+                           : launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], 1, grid, c->dtype == KVC_FP8_E4M3, c->d, st);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV attention launch");
     ++c->launches;
 

@@ -55,6 +55,8 @@ __host__ __device__ constexpr int key_tile_keys(int d, bool fp8) {
 }
 // FP8 E4M3 caches: one K and one V scale per KV head (at most this many heads).
 constexpr int kMaxScaleHeads = 64;
+// Keys per split-KV tile of 4-bit caches.
+constexpr int kQ4KeyTile = 128;
 
 // ---------------------------------------------------------------------------
 // In-place append: k_new/v_new [B, Hkv, T, d] -> cache rows lens[b] .. lens[b]+n_new[b]-1.
@@ -181,6 +183,7 @@ struct DecodeParams {
     // V reads code * vscale[h]; appended rows are quantized with 1/scale.
     float kscale[kMaxScaleHeads];
     float vscale[kMaxScaleHeads];
+    Q4Scales q4;             // 4-bit cache: the rows' scale words
     int prior[kMaxBatch];    // lens[b] - n_new[b]
     int n_new[kMaxBatch];
     int gstart[kMaxGroups + 1];
@@ -218,6 +221,9 @@ DecodeLaunch decode_launch_shape(int mt, bool fp8, int d);
 
 cudaError_t launch_decode_bf16(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int mt,
                                int grid, bool fp8, int d, cudaStream_t stream);
+// 4-bit caches: row blocks of p.RPB = 8 or 16, one partial sub-slot per (unit, CTA).
+cudaError_t launch_decode_q4(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid, int d,
+                             cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // f32 attention (any d <= 256, d % 4 == 0): one CTA per (16-row block, kvh, b),

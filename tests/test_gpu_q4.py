@@ -398,6 +398,117 @@ def test_layers_truncate_and_host_buffers():
     p.check_out(out, q, [2, 1], 3)
 
 
+@pytest.mark.parametrize("d,G,page", [(128, 4, 0), (64, 4, 0), (128, 8, 128), (128, 3, 0)])
+def test_device_steps_and_graph(d, G, page):
+    """Device-resident lengths: steps run eagerly and replayed from a graph, a rejected step, and the lengths back."""
+    p = Pair(3, 2, d, 256, page=page, seed=d + G)
+    p.step([100, 0, 126], G)
+    T = 2 if G * 2 <= 16 else 1
+    q, k, v = (torch.zeros(3, H, T, d, dtype=torch.bfloat16, device="cuda") for H in (2 * G, 2, 2))
+    n = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, ws = torch.zeros_like(q), torch.zeros(p.c.workspace_bytes(2 * G, T), dtype=torch.uint8, device="cuda")
+    p.c.lens_to_device()
+
+    def feed(n_new):
+        i = p.inputs(n_new, T, G)
+        for dst, src in zip((q, k, v), i):
+            dst.copy_(src)
+        n.copy_(torch.tensor(n_new, dtype=torch.int32))
+        return i
+
+    def check(i, n_new):
+        p.note(i[1], i[2], n_new)
+        K, V = p.values()
+        want, mass, dot = _attend(i[0].double().numpy(), K, V, p.lens, n_new)
+        got = out.double().cpu().numpy()
+        assert (np.abs(got - want) - _bound(want, mass, dot, G * T)).max() <= 0
+        assert p.c.device_status(ws) == 0
+
+    i = feed([T, 1, 0])
+    p.c.decode_step(0, q, k, v, n, out, ws)
+    check(i, [T, 1, 0])
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    feed([0, 0, 0])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        p.c.decode_step(0, q, k, v, n, out, ws)
+    for n_new in ([1, 1, T], [T, 0, 1], [0, T, T]):
+        i = feed(n_new)
+        graph.replay()
+        check(i, n_new)
+    feed([200, 0, 0] if T >= 200 else [T + 1, 0, 0])  # n_new outside 0 .. T: the whole step is rejected
+    graph.replay()
+    with pytest.raises(KVCError):
+        p.c.device_status(ws)
+    with pytest.raises(KVCError):
+        p.c.read(0, [0, 0, 0], [1, 1, 1])
+    p.c.lens_from_device()
+    assert np.array_equal(p.c.lens(0), p.lens)
+    p.check_store()
+    p.step([1, 1, 1], G)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_allocation_free_call(d):
+    p = Pair(3, 2, d, 300, seed=d)
+    p.step([100, 1, 260], 4)
+    for T in (1, 4):
+        q, k, v = p.inputs([T, 0, T], T, 4)
+        p.c.append(0, k.cuda(), v.cuda(), [T, 0, T])
+        p.note(k, v, [T, 0, T])
+        out = torch.empty_like(q, device="cuda")
+        p.c.gqa_attention_noalloc(0, q.cuda(), [T, 0, T], out=out)
+        assert p.c.noalloc_status() == 0
+        p.check_out(out, q, [T, 0, T], T)
+    c = KVCache(1, 1, 1, 64, 96, dtype="q4")
+    q = torch.zeros(1, 1, 1, 96, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(KVCError):  # the generic kernel's head widths have no such call, as for the other types
+        c.gqa_attention_noalloc(0, q, [0], out=q.clone())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hkv,G,L", [(1, 1, 8, 20000), (2, 8, 4, 5000), (40, 4, 2, 700), (5, 2, 16, 3001)])
+def test_longer_decode(d, B, Hkv, G, L):
+    """Units cut across many CTAs, whole units, and several units in one CTA."""
+    rng = np.random.default_rng(L)
+    p = Pair(B, Hkv, d, L + 8, seed=L)
+    n = rng.integers(L // 2, L + 1, size=B)
+    n[0] = L
+    if B > 2:
+        n[1] = 0
+    q, k, v = p.inputs(n, L, 1)
+    p.c.append(0, k.cuda(), v.cuda(), n)
+    p.note(k, v, n)
+    out = p.step(np.ones(B, dtype=np.int64), G)
+    p.c.truncate(p.lens)
+    q = p.inputs(np.ones(B), 1, G)[0].cuda()
+    a = p.c.gqa_attention(0, q, np.ones(B))
+    for _ in range(3):  # the same bits every time
+        assert torch.equal(a, p.c.gqa_attention(0, q, np.ones(B)))
+
+
+def test_streams_and_two_caches():
+    """Calls of two caches on two streams at once, each with its own workspace."""
+    a, b = Pair(2, 2, 128, 600, seed=1), Pair(2, 2, 64, 600, seed=2)
+    for p in (a, b):
+        p.step([500, 333], 4)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    work = []
+    for p, s in zip((a, b), streams):
+        i = p.inputs([1, 1], 1, 4)
+        gpu = [t.cuda() for t in i]
+        ws = torch.zeros(p.c.workspace_bytes(8, 1), dtype=torch.uint8, device="cuda")
+        work.append((p, s, i, gpu, ws, torch.empty_like(gpu[0])))
+    torch.cuda.synchronize()
+    for p, s, i, gpu, ws, out in work:
+        p.c.append_attention(0, *gpu, [1, 1], out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for p, s, i, gpu, ws, out in work:
+        p.note(i[1], i[2], [1, 1])
+        p.check_out(out, i[0], [1, 1], 1)
+
+
 def test_refusals():
     c = KVCache(1, 1, 1, 64, 128, dtype="q4")
     q = torch.zeros(1, 2, 1, 128, dtype=torch.bfloat16, device="cuda")
