@@ -45,14 +45,16 @@
 //
 // How (GB300).  One persistent CTA per SM; tiles of 128 keys (2 x 8 KB of codes
 // and 1 KB of scale words at d = 128) stream through TMA into a ring of stages;
-// every consumer warp takes 16 keys of a tile, eight warps a tile, and with
-// one block of 8 query rows two groups of eight warps take alternate tiles.
+// four warps share a tile, 32 keys each, and three groups of four (two with 16
+// query rows) take tiles in turn.
 // A unit's states meet in shared memory at its end, so a CTA leaves one
 // partial a unit.
 // Every wait is bounded in time; on expiry an error code is recorded.
 
 #include <cuda_fp16.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "kvc_internal.h"
 #include "ptx.cuh"
@@ -66,14 +68,16 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLazyRescale = 8.0f;  // log2 of the largest factor p may reach above the reference
 constexpr int kKT = kQ4KeyTile;       // keys per tile
-constexpr int kWarpKeys = 16;
+constexpr int kWarpKeys = 32;
 constexpr uint32_t kMinExp = 6;       // 2^(133 - 6) is the largest power of two of an fp32
 constexpr int kTileWarps = kKT / kWarpKeys;  // warps that share a tile
 
 // D: head width; QB: blocks of 8 query rows.
 template <int D, int QB>
 struct Q4Shape {
-    static constexpr int kGroups = QB == 1 ? 2 : 1;  // warp groups taking tiles in turn
+    // Warp groups taking tiles in turn: as many as leave a thread the registers
+    // it needs (128 with 12 consumer warps, 168 with 8).
+    static constexpr int kGroups = QB == 1 ? 3 : 2;
     static constexpr int kCW = kGroups * kTileWarps;
     static constexpr int kCT = kCW * 32;
     static constexpr int kThreads = kCT + 32;
@@ -84,7 +88,9 @@ struct Q4Shape {
     static constexpr int kPS = D + 4;              // floats of a state's row: O, m, l, pad
     static constexpr size_t kObuf = static_cast<size_t>(kCW) * kRows * kPS * sizeof(float);
     static constexpr int kFit = static_cast<int>((232448 - 1024 - 512 - kObuf) / kStageB);
-    static constexpr int kStages = kFit / 2 * 2 < 20 ? kFit / 2 * 2 : 20;  // even: a stage belongs to one group
+    // A multiple of the groups, so that a stage belongs to one of them and a
+    // stage's phases reach its warps in order.
+    static constexpr int kStages = (kFit < 20 ? kFit : 20) / kGroups * kGroups;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + 2 * kStages * 8 + 16;
     static_assert(kStageB % 1024 == 0, "stages keep the swizzle's alignment");
     static_assert(kSmem <= 232448, "shared memory per CTA");
@@ -162,6 +168,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     constexpr int KW = D / 32;   // 32-bit words of a thread's K codes a key (two MMA k-steps each)
     constexpr int VW = D / 64;   // 32-bit words of a thread's V codes a key (four 16-dim blocks each)
     constexpr int MB = D / 16;   // 16-dim blocks of O^T
+    constexpr int KB = kWarpKeys / 16;  // 16-key blocks of a slice
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -264,72 +271,70 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     }
 
     // ------------------------------------------------------------------ consumers
-    const int grp = warp / kTileWarps;                // tiles it with it % kGroups == grp
-    const int koff = (warp % kTileWarps) * kWarpKeys;  // this warp's keys of a tile
+    const int grp = warp / kTileWarps;                 // this warp's tiles: those of its group
+    const int koff = (warp % kTileWarps) * kWarpKeys;  // its keys of a tile
     const int quad = lane & 3, g = lane >> 2;
     const int kg = perm8<D>(g);                                    // K: key of accumulator row g (and + 8)
     const int va = perm8<D>(2 * quad), vb = perm8<D>(2 * quad + 1);  // V: keys of the k index 2 quad, 2 quad + 1
-    // Byte offsets of this thread's pieces in a tile (koff is a multiple of 16,
-    // so neither the swizzle nor the + 8 rows change them).
+    // Byte offsets of this thread's pieces in a tile (blocks start at multiples
+    // of 16 rows, so neither the swizzle nor the + 8 rows change them).
     const uint32_t kpiece = code_off<D>(kg, quad * (D / 8)) + koff * S::kRowB;
     const uint32_t vpiece_a = code_off<D>(va, (g * (D / 16)) & ~15) + ((g * (D / 16)) & 15) + koff * S::kRowB;
     const uint32_t vpiece_b = code_off<D>(vb, (g * (D / 16)) & ~15) + ((g * (D / 16)) & 15) + koff * S::kRowB;
 
     Cursor<DP, kKT> cur;
     cur.init(wp, x0);
+    int mine = grp, stage = grp, phase = 0;  // this warp's next tile of the CTA's sequence, its stage and parity
 
-    float o[QB][MB][4];
-    float m[QB][2], l[QB][2], zs[QB][2];   // of query rows 8 nb + 2 quad, + 1: maximum, sum, zero points' sum
-    float rs[QB][2], qs[QB][2];            // their score factor and sum of scaled q
-    int lim[QB][2];                        // last visible key (-1: no such query)
-    uint32_t qa[QB][2 * KW][2];
-    uint32_t vexp = kMinExp;               // exponent field of the largest V step met (at least kMinExp)
-    float vmul = 0.f;                      // 2^(133 - vexp)
-    int min_lim = 0, extent = 0, seg_j0 = 0, seg_prior = 0, seg_nn = 0, max_lo = -1, min_lo = -1;
+    for (int x = x0; x < x1;) {
+        // One segment: this CTA's tiles of one unit.
+        const int b = cur.q / p.RB, rb = cur.q - b * p.RB, kvh = cur.kvh, j0 = cur.j;
+        const int nseg = min(cur.nt - j0, x1 - x);
+        const int it_end = x - x0 + nseg;
+        const int prior = wp.prior(b), nn = wp.n_new(b);
+        int extent, min_lim;
+        block_bounds(wp, b, rb, extent, min_lim);
+        const int max_lo = p.window > 0 ? extent - 1 - p.window : -1;  // keys > max_lo are in every query's window
+        const int min_lo = p.window > 0 ? min_lim - p.window : -1;     // keys <= min_lo in none
+        const int seg_key0 = (cur.t0 + j0) * kKT + koff - (x - x0) * kKT;  // + it * kKT: the slice's first key
 
-    for (int x = x0, it = 0; x < x1; ++x, ++it) {
-        const int s = it % kStages;
-        const int b = cur.q / p.RB, rb = cur.q - (cur.q / p.RB) * p.RB;
-        const int j = cur.j, nt = cur.nt, kvh = cur.kvh;
-
-        if (x == x0 || j == 0) {
-            // New unit segment: bounds, query fragments, fresh state.
-            seg_prior = wp.prior(b);
-            seg_nn = wp.n_new(b);
-            block_bounds(wp, b, rb, extent, min_lim);
-            max_lo = (p.window > 0 && extent > 0) ? extent - 1 - p.window : -1;
-            min_lo = (p.window > 0 && extent > 0) ? min_lim - p.window : -1;
-            seg_j0 = j;
-            vexp = kMinExp;
-            vmul = __uint_as_float((260u - kMinExp) << 23);
+        // Query fragments: this thread holds query row g's dims quad * D / 4 ..,
+        // word by word; the k-steps of a word take its value pairs (0, 1), (2, 3)
+        // and (4, 5), (6, 7), whose codes come as c 2^-24 and c 2^-20 in turn.
+        // All rows are scaled by one power of two, 2^(141 - e), e the exponent
+        // field of the largest |q|.
+        uint32_t qa[QB][2 * KW][2];
+        float qs[QB][2];   // sums of the scaled q of query rows 8 nb + 2 quad, + 1, times 2^-24
+        float rs;          // scores' factor: 2^(e - 141) 2^24 log2(e) / sqrt(d)
+        int lim[QB][2];    // last visible key (-1: no such query)
+        {
+            uint4 w[QB][KW];
+            uint32_t top = 0;
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb) {
-                // q fragments: this thread holds query row g's dims
-                // quad * D / 4 .., word by word; the k-steps of a word take its
-                // value pairs (0, 1), (2, 3) and (4, 5), (6, 7), whose codes
-                // come as c 2^-24 and c 2^-20 in turn.
                 const int r = rb * p.RPB + nb * 8 + g;
-                const __nv_bfloat16* qrow = nullptr;
+                const uint4* qrow = nullptr;
                 if (r < p.R)
-                    qrow = static_cast<const __nv_bfloat16*>(p.q) +
-                           ((static_cast<size_t>(b) * p.Hq + kvh * p.G + r / p.T) * p.T + r % p.T) * D + quad * (D / 4);
-                uint4 w[KW];
-                uint32_t top = 0;
+                    qrow = reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(p.q) +
+                        ((static_cast<size_t>(b) * p.Hq + kvh * p.G + r / p.T) * p.T + r % p.T) * D + quad * (D / 4));
 #pragma unroll
                 for (int i = 0; i < KW; ++i) {
-                    w[i] = qrow ? __ldg(reinterpret_cast<const uint4*>(qrow) + i) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    w[nb][i] = qrow ? __ldg(qrow + i) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t u[4] = {w[nb][i].x, w[nb][i].y, w[nb][i].z, w[nb][i].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+                    for (int c = 0; c < 4; ++c) top = max(top, max(u[c] & 0x7FFFu, (u[c] >> 16) & 0x7FFFu));
                 }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = max(14, static_cast<int>(top >> 7));  // exponent field of the row's largest |q|
-                const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
+            }
+            const int e = max(14, static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7));
+            const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+            rs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23);
+#pragma unroll
+            for (int nb = 0; nb < QB; ++nb) {
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < KW; ++i) {
-                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    const uint32_t u[4] = {w[nb][i].x, w[nb][i].y, w[nb][i].z, w[nb][i].w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float a0 = __uint_as_float(u[c] << 16) * f, a1 = __uint_as_float(u[c] & 0xFFFF0000u) * f;
@@ -340,98 +345,58 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                const float rowf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23);  // 2^(e - 141 + 24)
-                // ... and the factors of the rows this thread's accumulators stand for
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     qs[nb][h] = __shfl_sync(0xffffffffu, sum, (2 * quad + h) * 4) * 5.9604644775390625e-8f;  // 2^-24
-                    rs[nb][h] = __shfl_sync(0xffffffffu, rowf, (2 * quad + h) * 4);
-                    const int rr = rb * p.RPB + nb * 8 + 2 * quad + h, t = rr % p.T;
-                    lim[nb][h] = (rr < p.R && t < seg_nn) ? seg_prior + t : -1;
-                    m[nb][h] = -INFINITY;
-                    l[nb][h] = 0.f;
-                    zs[nb][h] = 0.f;
+                    const int r = rb * p.RPB + nb * 8 + 2 * quad + h, t = r % p.T;
+                    lim[nb][h] = (r < p.R && t < nn) ? prior + t : -1;
                 }
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) o[nb][mb][0] = o[nb][mb][1] = o[nb][mb][2] = o[nb][mb][3] = 0.f;
             }
         }
 
-        if (S::kGroups == 1 || (it % S::kGroups) == grp) {
-            // On expiry the warp records the error and carries on with whatever
-            // the stage holds (the call's output is then invalid): consumer
-            // warps meet at named barriers, so none may leave the loop alone.
-            if (!ptx::mbar_wait_bounded(bar0 + 8 * s, (it / kStages) & 1, *abort_flag ? 0ull : kWaitLimitNs)) {
-                atomicExch(p.err, kDevTimeoutFull);
-                *abort_flag = 1;
-            }
-            const uint32_t sK = stage0 + s * S::kStageB, sV = sK + S::kCodeB, sS = sV + S::kCodeB;
-            const int key0 = (cur.t0 + j) * kKT + koff;  // first key position of this warp's slice
-
-            if (p.append_new) {
-                // In-kernel append: the chunk's rows that fall into this slice are
-                // quantised here, patched into the staged tile (whose copy of
-                // them is stale) and written to the cache.  Half a warp takes K
-                // and half V, eight values a lane.
-                const int lo = max(seg_prior, key0), hi = min(seg_prior + seg_nn, key0 + kWarpKeys);
-                for (int pos = lo; pos < hi; ++pos) {
-                    const bool is_v = lane >= 16;
-                    const int c = lane & 15, r = pos - key0 + koff;
-                    const bool live = c < D / 8;
-                    const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_new : p.k_new) +
-                                         ((static_cast<size_t>(b) * p.Hkv + kvh) * p.Tn + (pos - seg_prior)) * (D * 2);
-                    const uint4 val = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {val.x, val.y, val.z, val.w};
-                    float a, z;
-                    q4::range8(w, a, z);
+        // The segment's state.
+        float o[QB][MB][4];
+        float m[QB][2], nm[QB][2], l[QB][2], zs[QB][2];  // rows' maximum (and its negative, 0 before any), sums of p, of p s_v z_v
+        uint32_t vexp = kMinExp;                          // exponent field of the largest V step met (at least kMinExp)
+        float vmul = __uint_as_float((260u - kMinExp) << 23);  // 2^(133 - vexp)
 #pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) {
-                        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, d));
-                    }
-                    const q4::RowScale sc = q4::row_scale(a, z);
-                    const uint32_t code = q4::encode8(w, sc);
-                    bool bad = false;
-                    const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, kvh, pos, &bad);
-                    uint8_t* stg = smem + s * S::kStageB + (is_v ? S::kCodeB : 0);
-                    uint8_t* words = smem + s * S::kStageB + 2 * S::kCodeB + (is_v ? kKT * 4 : 0);
-                    if (live) {
-                        *reinterpret_cast<uint32_t*>(stg + code_off<D>(r, (c * 4) & ~15) + ((c * 4) & 15)) = code;
-                        if (!bad)
-                            reinterpret_cast<uint32_t*>(is_v ? p.v_cache : p.k_cache)[static_cast<size_t>(row) * (D / 8) + c] =
-                                code;
-                    }
-                    if (c == 0) {
-                        *reinterpret_cast<uint32_t*>(words + r * 4) = sc.word;
-                        if (!bad) (is_v ? p.q4.v : p.q4.k)[q4::scale_index(p.q4, row)] = sc.word;
-                    }
-                }
-                if (lo < hi) {
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                }
+        for (int nb = 0; nb < QB; ++nb) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[nb][h] = -INFINITY;
+                nm[nb][h] = l[nb][h] = zs[nb][h] = 0.f;
             }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) o[nb][mb][0] = o[nb][mb][1] = o[nb][mb][2] = o[nb][mb][3] = 0.f;
+        }
 
-            if (key0 < extent && key0 + kWarpKeys - 1 > min_lo) {
-                const bool full = key0 + kWarpKeys - 1 <= min_lim && key0 > max_lo && (!TREE || key0 + kWarpKeys <= seg_prior);
-                // S^T = K q^T: 16 keys x 8 QB query rows.
+        // One slice of kWarpKeys keys from key0 on, staged at sK / sV / sS.
+        // FULL: every valid query of the block sees every key of it.
+        auto attend = [&](auto full_tag, const int key0, const uint32_t sK, const uint32_t sV, const uint32_t sS) {
+            constexpr bool FULL = decltype(full_tag)::value;
+            // S^T = K q^T: blocks of 16 keys x 8 query rows.
+            float sc[KB][QB][4];
+            uint32_t kw[KB][2], vw[KB][2];
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    kw[kb][h] = lds32(sS + (koff + kb * 16 + kg + 8 * h) * 4);
+                    vw[kb][h] = lds32(sS + (kKT + koff + kb * 16 + kg + 8 * h) * 4);
+                }
                 uint32_t k0w[KW], k1w[KW];
+                const uint32_t ka = sK + kpiece + kb * 16 * S::kRowB;
                 if constexpr (D == 128) {
-                    const uint4 a = ptx::ld_shared_v4(sK + kpiece), c = ptx::ld_shared_v4(sK + kpiece + 8 * S::kRowB);
-                    k0w[0] = a.x, k0w[1] = a.y, k0w[2] = a.z, k0w[3] = a.w;
-                    k1w[0] = c.x, k1w[1] = c.y, k1w[2] = c.z, k1w[3] = c.w;
+                    const uint4 u = ptx::ld_shared_v4(ka), v = ptx::ld_shared_v4(ka + 8 * S::kRowB);
+                    k0w[0] = u.x, k0w[1] = u.y, k0w[2] = u.z, k0w[3] = u.w;
+                    k1w[0] = v.x, k1w[1] = v.y, k1w[2] = v.z, k1w[3] = v.w;
                 } else {
-                    const uint2 a = lds64(sK + kpiece), c = lds64(sK + kpiece + 8 * S::kRowB);
-                    k0w[0] = a.x, k0w[1] = a.y;
-                    k1w[0] = c.x, k1w[1] = c.y;
+                    const uint2 u = lds64(ka), v = lds64(ka + 8 * S::kRowB);
+                    k0w[0] = u.x, k0w[1] = u.y;
+                    k1w[0] = v.x, k1w[1] = v.y;
                 }
-                uint32_t kw[2] = {lds32(sS + (koff + kg) * 4), lds32(sS + (koff + kg + 8) * 4)};
-                uint32_t vw[2] = {lds32(sS + (kKT + koff + kg) * 4), lds32(sS + (kKT + koff + kg + 8) * 4)};
-                float sc[QB][4], sd[QB][4];  // two chains of products, for their latency
 #pragma unroll
-                for (int nb = 0; nb < QB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nb][e] = sd[nb][e] = 0.f;
+                for (int nb = 0; nb < QB; ++nb) sc[kb][nb][0] = sc[kb][nb][1] = sc[kb][nb][2] = sc[kb][nb][3] = 0.f;
 #pragma unroll
                 for (int i = 0; i < KW; ++i) {
                     const uint32_t x0w = k0w[i], x1w = k1w[i], y0w = x0w >> 8, y1w = x1w >> 8;
@@ -439,90 +404,102 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     const uint32_t c[4] = {y0w & 0x000F000Fu, y1w & 0x000F000Fu, y0w & 0x00F000F0u, y1w & 0x00F000F0u};
 #pragma unroll
                     for (int nb = 0; nb < QB; ++nb) {
-                        ptx::mma_f16_16816(sc[nb], a, qa[nb][2 * i][0], qa[nb][2 * i][1]);
-                        ptx::mma_f16_16816(sd[nb], c, qa[nb][2 * i + 1][0], qa[nb][2 * i + 1][1]);
+                        ptx::mma_f16_16816(sc[kb][nb], a, qa[nb][2 * i][0], qa[nb][2 * i][1]);
+                        ptx::mma_f16_16816(sc[kb][nb], c, qa[nb][2 * i + 1][0], qa[nb][2 * i + 1][1]);
                     }
                 }
-                // Keys that no query of the block sees: no step, so that neither
-                // a stale word nor its exponent enters.
-                const int kp[2] = {key0 + kg, key0 + kg + 8};
-                if (!full) {
+            }
+            // Scores in base 2, masked; each row's maximum over the slice.  Keys
+            // that no query of the block sees get no step, so that neither a
+            // stale word nor its exponent enters.
+            float mx[QB][2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (kp[h] >= extent || kp[h] <= min_lo) kw[h] = vw[h] = 0u;
+            for (int nb = 0; nb < QB; ++nb) mx[nb][0] = mx[nb][1] = -INFINITY;
+            uint32_t ve = 0;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = key0 + kb * 16 + kg + 8 * h;
+                    if (!FULL && (key >= extent || key <= min_lo)) kw[kb][h] = vw[kb][h] = 0u;
+                    const uint32_t ex = vw[kb][h] >> 23;
+                    ve = max(ve, ex == 255u ? 0u : ex);  // (a NaN step stays NaN under any factor)
+                    const float ks = q4::step_of(kw[kb][h]) * rs, kz = -small_to_f32(kw[kb][h] & 0xFFFFu);
+#pragma unroll
+                    for (int nb = 0; nb < QB; ++nb)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float& v = sc[kb][nb][2 * h + c];
+                            v = fmaf(kz, qs[nb][c], v) * ks;
+                            if (!FULL) {
+                                const int li = lim[nb][c];
+                                bool see = key <= li && (p.window <= 0 || key > li - p.window);
+                                if (TREE && see && key >= prior) see = (p.anc[b * p.T + (li - prior)] >> (key - prior)) & 1ull;
+                                if (!see) v = -INFINITY;
+                            }
+                            mx[nb][c] = fmaxf(mx[nb][c], v);
+                        }
                 }
-                // Scores in base 2, masked; each row's maximum over the 16 keys.
-                const float ks0 = q4::step_of(kw[0]), ks1 = q4::step_of(kw[1]);
-                const float kz0 = small_to_f32(kw[0] & 0xFFFFu), kz1 = small_to_f32(kw[1] & 0xFFFFu);
-                float mx[QB][2];
-                bool move = false;
+            }
+            bool move = ve > vexp;
+#pragma unroll
+            for (int nb = 0; nb < QB; ++nb)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float t = mx[nb][c];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    mx[nb][c] = t;
+                    move |= t > m[nb][c] + kLazyRescale;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+                // Move the references; O, l and the zero points' sum follow.
+                ve = max(vexp, __reduce_max_sync(0xffffffffu, ve));
+                const float fv =
+                    __uint_as_float(static_cast<uint32_t>(max(0, 127 + static_cast<int>(vexp) - static_cast<int>(ve))) << 23);
+                vexp = ve;
+                vmul = __uint_as_float((260u - vexp) << 23);
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
+                    float f[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float raw = sc[nb][e] + sd[nb][e];
-                        sc[nb][e] = fmaf(-((e < 2) ? kz0 : kz1), qs[nb][e & 1], raw) * rs[nb][e & 1] * ((e < 2) ? ks0 : ks1);
-                        if (!full) {
-                            const int key = kp[e >> 1], li = lim[nb][e & 1];
-                            bool see = key <= li && (p.window <= 0 || key > li - p.window);
-                            if (TREE && see && key >= seg_prior)
-                                see = (p.anc[b * p.T + (li - seg_prior)] >> (key - seg_prior)) & 1ull;
-                            if (!see) sc[nb][e] = -INFINITY;
+                    for (int c = 0; c < 2; ++c) {
+                        const bool mv = mx[nb][c] > m[nb][c] + kLazyRescale;
+                        const float al = !mv ? 1.f : (m[nb][c] == -INFINITY) ? 0.f : ptx::ex2(m[nb][c] - mx[nb][c]);
+                        if (mv) {
+                            m[nb][c] = mx[nb][c];
+                            nm[nb][c] = -mx[nb][c];
                         }
+                        l[nb][c] *= al;
+                        f[c] = al * fv;
+                        zs[nb][c] *= f[c];
                     }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float t = fmaxf(sc[nb][h], sc[nb][2 + h]);
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                        mx[nb][h] = t;
-                        move |= t > m[nb][h] + kLazyRescale;
-                    }
-                }
-                uint32_t ve = max((vw[0] >> 23) == 255u ? 0u : vw[0] >> 23, (vw[1] >> 23) == 255u ? 0u : vw[1] >> 23);
-                if (__any_sync(0xffffffffu, move || ve > vexp)) {
-                    // Move the references; O, l and the zero points' sum follow.
-                    ve = max(vexp, __reduce_max_sync(0xffffffffu, ve));
-                    const float fv = __uint_as_float(static_cast<uint32_t>(max(0, 127 + static_cast<int>(vexp) - static_cast<int>(ve))) << 23);
-                    vexp = ve;
-                    vmul = __uint_as_float((260u - vexp) << 23);
-#pragma unroll
-                    for (int nb = 0; nb < QB; ++nb) {
-                        float f[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const bool mv = mx[nb][h] > m[nb][h] + kLazyRescale;
-                            const float al = !mv ? 1.f : (m[nb][h] == -INFINITY) ? 0.f : ptx::ex2(m[nb][h] - mx[nb][h]);
-                            if (mv) m[nb][h] = mx[nb][h];
-                            l[nb][h] *= al;
-                            f[h] = al * fv;
-                            zs[nb][h] *= f[h];
-                        }
-#pragma unroll
-                        for (int mb = 0; mb < MB; ++mb) {
-                            o[nb][mb][0] *= f[0];
-                            o[nb][mb][1] *= f[1];
-                            o[nb][mb][2] *= f[0];
-                            o[nb][mb][3] *= f[1];
-                        }
+                    for (int mb = 0; mb < MB; ++mb) {
+                        o[nb][mb][0] *= f[0];
+                        o[nb][mb][1] *= f[1];
+                        o[nb][mb][2] *= f[0];
+                        o[nb][mb][3] *= f[1];
                     }
                 }
-                // Weights: p into l, p s_v (f16) into the products, times z_v
-                // into the zero points' sum.
-                const float vs0 = q4::step_of(vw[0]) * vmul, vs1 = q4::step_of(vw[1]) * vmul;
-                const float vz0 = small_to_f32(vw[0] & 0xFFFFu), vz1 = small_to_f32(vw[1] & 0xFFFFu);
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                // Weights: p into l, p s_v (f16) into the products, times z_v into
+                // the zero points' sum.
+                const float vs0 = q4::step_of(vw[kb][0]) * vmul, vs1 = q4::step_of(vw[kb][1]) * vmul;
+                const float vz0 = small_to_f32(vw[kb][0] & 0xFFFFu), vz1 = small_to_f32(vw[kb][1] & 0xFFFFu);
                 uint32_t pb[QB][2];
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
                     float pw[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float mu = m[nb][e & 1];
-                        const float pe = ptx::ex2(sc[nb][e] - (mu == -INFINITY ? 0.f : mu));
+                        const float v = sc[kb][nb][e], pe = ptx::ex2(v + nm[nb][e & 1]);
                         l[nb][e & 1] += pe;
                         pw[e] = pe * ((e < 2) ? vs0 : vs1);
-                        if (!full && sc[nb][e] == -INFINITY) pw[e] = 0.f;  // (a NaN step this query does not see)
+                        if (!FULL && v == -INFINITY) pw[e] = 0.f;  // (a NaN step that this query does not see)
                     }
                     const uint32_t h0 = ptx::pack_f16x2(pw[0], pw[1]), h1 = ptx::pack_f16x2(pw[2], pw[3]);
                     const float2 r0 = f16x2_to_f32(h0), r1 = f16x2_to_f32(h1);
@@ -533,14 +510,15 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                 }
                 // O^T += V^T P^T.
                 uint32_t va0[VW], vb0[VW], va8[VW], vb8[VW];
+                const uint32_t pa = sV + vpiece_a + kb * 16 * S::kRowB, pc = sV + vpiece_b + kb * 16 * S::kRowB;
                 if constexpr (D == 128) {
-                    const uint2 t0 = lds64(sV + vpiece_a), t1 = lds64(sV + vpiece_b);
-                    const uint2 t2 = lds64(sV + vpiece_a + 8 * S::kRowB), t3 = lds64(sV + vpiece_b + 8 * S::kRowB);
+                    const uint2 t0 = lds64(pa), t1 = lds64(pc);
+                    const uint2 t2 = lds64(pa + 8 * S::kRowB), t3 = lds64(pc + 8 * S::kRowB);
                     va0[0] = t0.x, va0[1] = t0.y, vb0[0] = t1.x, vb0[1] = t1.y;
                     va8[0] = t2.x, va8[1] = t2.y, vb8[0] = t3.x, vb8[1] = t3.y;
                 } else {
-                    va0[0] = lds32(sV + vpiece_a), vb0[0] = lds32(sV + vpiece_b);
-                    va8[0] = lds32(sV + vpiece_a + 8 * S::kRowB), vb8[0] = lds32(sV + vpiece_b + 8 * S::kRowB);
+                    va0[0] = lds32(pa), vb0[0] = lds32(pc);
+                    va8[0] = lds32(pa + 8 * S::kRowB), vb8[0] = lds32(pc + 8 * S::kRowB);
                 }
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
@@ -559,13 +537,80 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     }
                 }
             }
+        };
+
+        for (; mine < it_end; mine += S::kGroups) {
+            // On expiry the warp records the error and carries on with whatever
+            // the stage holds (the call's output is then invalid): consumer
+            // warps meet at named barriers, so none may leave the loop alone.
+            if (!ptx::mbar_try_wait(bar0 + 8 * stage, phase) &&
+                !ptx::mbar_wait_bounded(bar0 + 8 * stage, phase, *abort_flag ? 0ull : kWaitLimitNs)) {
+                atomicExch(p.err, kDevTimeoutFull);
+                *abort_flag = 1;
+            }
+            const uint32_t sK = stage0 + stage * S::kStageB, sV = sK + S::kCodeB, sS = sV + S::kCodeB;
+            const int key0 = seg_key0 + mine * kKT;
+
+            if (p.append_new && key0 + kWarpKeys > prior) {
+                // In-kernel append: the chunk's rows that fall into this slice are
+                // quantised here, patched into the staged tile (whose copy of
+                // them is stale) and written to the cache.  Half a warp takes K
+                // and half V, eight values a lane.
+                const int lo = max(prior, key0), hi = min(prior + nn, key0 + kWarpKeys);
+                for (int pos = lo; pos < hi; ++pos) {
+                    const bool is_v = lane >= 16;
+                    const int c = lane & 15, r = pos - key0 + koff;
+                    const bool live = c < D / 8;
+                    const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_new : p.k_new) +
+                                         ((static_cast<size_t>(b) * p.Hkv + kvh) * p.Tn + (pos - prior)) * (D * 2);
+                    const uint4 val = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t w[4] = {val.x, val.y, val.z, val.w};
+                    float a, z;
+                    q4::range8(w, a, z);
+#pragma unroll
+                    for (int d = 8; d > 0; d >>= 1) {
+                        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, d));
+                    }
+                    const q4::RowScale sc = q4::row_scale(a, z);
+                    const uint32_t code = q4::encode8(w, sc);
+                    bool bad = false;
+                    const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, kvh, pos, &bad);
+                    uint8_t* stg = smem + stage * S::kStageB + (is_v ? S::kCodeB : 0);
+                    uint8_t* words = smem + stage * S::kStageB + 2 * S::kCodeB + (is_v ? kKT * 4 : 0);
+                    if (live) {
+                        *reinterpret_cast<uint32_t*>(stg + code_off<D>(r, (c * 4) & ~15) + ((c * 4) & 15)) = code;
+                        if (!bad)
+                            reinterpret_cast<uint32_t*>(is_v ? p.v_cache : p.k_cache)[static_cast<size_t>(row) * (D / 8) + c] =
+                                code;
+                    }
+                    if (c == 0) {
+                        *reinterpret_cast<uint32_t*>(words + r * 4) = sc.word;
+                        if (!bad) (is_v ? p.q4.v : p.q4.k)[q4::scale_index(p.q4, row)] = sc.word;
+                    }
+                }
+                if (lo < hi) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+
+            if (key0 + kWarpKeys - 1 <= min_lim && key0 > max_lo && (!TREE || key0 + kWarpKeys <= prior))
+                attend(std::true_type(), key0, sK, sV, sS);
+            else if (key0 < extent && key0 + kWarpKeys - 1 > min_lo)
+                attend(std::false_type(), key0, sK, sV, sS);
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar0 + 8 * (kStages + s));
+            if (lane == 0) ptx::mbar_arrive(bar0 + 8 * (kStages + stage));
+            stage += S::kGroups;
+            if (stage >= kStages) {
+                stage -= kStages;
+                phase ^= 1;
+            }
         }
 
-        if (x == x1 - 1 || j == nt - 1) {
-            // The segment's end: every warp's state of every query row into
-            // shared memory, O in real units.
+        // The segment's end: every warp's state of every query row into shared
+        // memory, O in real units.
+        {
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb)
 #pragma unroll
@@ -602,14 +647,14 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             ptx::named_barrier_sync(1, S::kCT);
             // Merge them in the order of the warps, and write the unit's output
             // (this CTA saw all of it) or the CTA's partial.
-            const bool sole = seg_j0 == 0 && j == nt - 1;
+            const bool sole = nseg == cur.nt;
             constexpr int C4 = D / 4;
             for (int idx = tid; idx < S::kRows * C4; idx += S::kCT) {
                 const int lr = idx / C4, c4 = idx - lr * C4;
                 const int r = rb * p.RPB + lr;
                 if (r >= p.R) continue;
                 const int t = r % p.T;
-                if (t >= seg_nn) continue;
+                if (t >= nn) continue;
                 const float* st = obuf + lr * PS;
                 float M = -INFINITY;
 #pragma unroll
@@ -648,7 +693,9 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             }
             ptx::named_barrier_sync(1, S::kCT);
         }
-        cur.advance(wp);
+        x += nseg;
+        cur.j = cur.nt - 1;  // (the next unit; past the last one nothing reads it)
+        if (x < x1) cur.advance(wp);
     }
 }
 
