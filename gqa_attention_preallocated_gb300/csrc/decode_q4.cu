@@ -28,8 +28,8 @@
 //    match in q's fragments.
 //  * V: a thread's output dims are one 8-byte (4-byte) piece of each key's row;
 //    two keys' words are woven into f16 pairs by a byte permute.
-//  * The 8 keys of a block are read in the order kPerm, which puts both
-//    accesses on distinct shared-memory banks (checked for every phase).
+//  * The 8 keys of a block are read in the order perm8, which puts K's accesses
+//    on distinct shared-memory banks and V's at most two to a bank (d = 128).
 //
 // Range.  q is scaled by a power of two to just below 2^15 a row, so that f16
 // holds it exactly whatever its size.  Weights are f16 too: p s_v 2^(133 - e),
@@ -44,7 +44,7 @@
 // clearing.
 //
 // How (GB300).  One persistent CTA per SM; tiles of 128 keys (2 x 8 KB of codes
-// and 1 KB of scale words at d = 128) stream through TMA into a ring of stages;
+// and 1 KB of scale words at d = 128) stream through bulk copies into a ring of stages;
 // four warps share a tile, 32 keys each, and three groups of four (two with 16
 // query rows) take tiles in turn.
 // A unit's states meet in shared memory at its end, so a CTA leaves one
@@ -92,7 +92,6 @@ struct Q4Shape {
     // stage's phases reach its warps in order.
     static constexpr int kStages = (kFit < 20 ? kFit : 20) / kGroups * kGroups;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + 2 * kStages * 8 + 16;
-    static_assert(kStageB % 1024 == 0, "stages keep the swizzle's alignment");
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -100,14 +99,6 @@ struct Q4Shape {
 template <int D>
 __device__ __forceinline__ int perm8(int i) {
     return ((D == 128 ? 0x67235410u : 0x67453210u) >> (4 * i)) & 7;
-}
-
-// Byte offset of 16-byte piece `c` of row r of a tile of 64-byte rows under the
-// 64-byte swizzle (d = 64: 32-byte rows, not swizzled).
-template <int D>
-__device__ __forceinline__ uint32_t code_off(int r, int byte) {
-    if constexpr (D == 128) return r * 64 + (byte ^ (((r >> 1) & 3) << 4));
-    return r * 32 + byte;
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -160,8 +151,7 @@ __device__ __forceinline__ void block_bounds(const Part<DP>& w, int b, int rb, i
 // DP: the partition comes from a device plan; TREE: draft-tree ancestor masks.
 template <int D, int QB, bool DP, bool TREE>
 __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
-    decode_q4_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV) {
+    decode_q4_kernel(const __grid_constant__ DecodeParams p) {
     using S = Q4Shape<D, QB>;
     constexpr int kStages = S::kStages;
     constexpr int PS = S::kPS;
@@ -192,10 +182,6 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
         }
         *abort_flag = 0;
         ptx::fence_barrier_init();
-    }
-    if (warp == S::kCW && lane == 0) {
-        ptx::tma_prefetch_desc(&tmK);
-        ptx::tma_prefetch_desc(&tmV);
     }
     __syncthreads();
     ptx::grid_dependency_wait();
@@ -239,20 +225,18 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     }
                 }
                 if (*abort_flag) break;  // the producer is in no named barrier, so it may stop early
+                // The tile's rows lie behind one another: one copy each of K, of
+                // V and of their scale words, up to the last visible key (scale
+                // words to the next multiple of 4, which the unit's stride holds).
                 const int tile0 = (cur.t0 + cur.j) * kKT;
                 const int row = key_row(p, b, cur.kvh, tile0);
+                const int n = min(kKT, extent - tile0);
                 const uint32_t full = bar0 + 8 * s, sK = stage0 + s * S::kStageB, sV = sK + S::kCodeB;
-                // Scale words: as many as the unit still has (its stride is a
-                // multiple of 4 words, so the copy keeps to 16 bytes).
-                const int unit = row / p.q4.tokens, off = row - unit * p.q4.tokens;
-                const size_t sidx = static_cast<size_t>(unit) * p.q4.stride + off;
-                const uint32_t sbytes = min(kKT, p.q4.stride - off) * 4;
-                const int boxes = extent - tile0 > kKT / 2 ? 2 : 1;  // 64-key halves that hold visible keys
-                ptx::mbar_arrive_expect_tx(full, boxes * S::kCodeB + 2 * sbytes);
-                for (int h = 0; h < boxes; ++h) {
-                    ptx::tma_load_2d(sK + h * (S::kCodeB / 2), &tmK, 0, row + h * (kKT / 2), full);
-                    ptx::tma_load_2d(sV + h * (S::kCodeB / 2), &tmV, 0, row + h * (kKT / 2), full);
-                }
+                const size_t sidx = q4::scale_index(p.q4, row), bytes = static_cast<size_t>(row) * S::kRowB;
+                const uint32_t sbytes = (n + 3) / 4 * 16;
+                ptx::mbar_arrive_expect_tx(full, 2 * (n * S::kRowB + sbytes));
+                bulk_load(sK, static_cast<const uint8_t*>(p.k_cache) + bytes, n * S::kRowB, full);
+                bulk_load(sV, static_cast<const uint8_t*>(p.v_cache) + bytes, n * S::kRowB, full);
                 bulk_load(sV + S::kCodeB, p.q4.k + sidx, sbytes, full);
                 bulk_load(sV + S::kCodeB + kKT * 4, p.q4.v + sidx, sbytes, full);
                 ++issued;
@@ -276,11 +260,10 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     const int quad = lane & 3, g = lane >> 2;
     const int kg = perm8<D>(g);                                    // K: key of accumulator row g (and + 8)
     const int va = perm8<D>(2 * quad), vb = perm8<D>(2 * quad + 1);  // V: keys of the k index 2 quad, 2 quad + 1
-    // Byte offsets of this thread's pieces in a tile (blocks start at multiples
-    // of 16 rows, so neither the swizzle nor the + 8 rows change them).
-    const uint32_t kpiece = code_off<D>(kg, quad * (D / 8)) + koff * S::kRowB;
-    const uint32_t vpiece_a = code_off<D>(va, (g * (D / 16)) & ~15) + ((g * (D / 16)) & 15) + koff * S::kRowB;
-    const uint32_t vpiece_b = code_off<D>(vb, (g * (D / 16)) & ~15) + ((g * (D / 16)) & 15) + koff * S::kRowB;
+    // Byte offsets of this thread's pieces in a tile.
+    const uint32_t kpiece = (koff + kg) * S::kRowB + quad * (D / 8);
+    const uint32_t vpiece_a = (koff + va) * S::kRowB + g * (D / 16);
+    const uint32_t vpiece_b = (koff + vb) * S::kRowB + g * (D / 16);
 
     Cursor<DP, kKT> cur;
     cur.init(wp, x0);
@@ -579,7 +562,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     uint8_t* stg = smem + stage * S::kStageB + (is_v ? S::kCodeB : 0);
                     uint8_t* words = smem + stage * S::kStageB + 2 * S::kCodeB + (is_v ? kKT * 4 : 0);
                     if (live) {
-                        *reinterpret_cast<uint32_t*>(stg + code_off<D>(r, (c * 4) & ~15) + ((c * 4) & 15)) = code;
+                        *reinterpret_cast<uint32_t*>(stg + r * S::kRowB + c * 4) = code;
                         if (!bad)
                             reinterpret_cast<uint32_t*>(is_v ? p.v_cache : p.k_cache)[static_cast<size_t>(row) * (D / 8) + c] =
                                 code;
@@ -700,8 +683,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 }
 
 template <int D, int QB, bool DP, bool TREE>
-cudaError_t launch_q4_t(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid,
-                        cudaStream_t stream) {
+cudaError_t launch_q4_t(const DecodeParams& p, int grid, cudaStream_t stream) {
     using S = Q4Shape<D, QB>;
     static bool attr_set = false;
     if (!attr_set) {
@@ -710,28 +692,25 @@ cudaError_t launch_q4_t(const DecodeParams& p, const CUtensorMap& tmK, const CUt
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    cudaError_t e = launch_pdl(decode_q4_kernel<D, QB, DP, TREE>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p, tmK, tmV);
+    cudaError_t e = launch_pdl(decode_q4_kernel<D, QB, DP, TREE>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 template <int D, int QB>
-cudaError_t launch_q4_shape(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid,
-                            cudaStream_t stream) {
-    if (p.dplan) return p.anc ? cudaErrorInvalidValue : launch_q4_t<D, QB, true, false>(p, tmK, tmV, grid, stream);
-    return p.anc ? launch_q4_t<D, QB, false, true>(p, tmK, tmV, grid, stream)
-                 : launch_q4_t<D, QB, false, false>(p, tmK, tmV, grid, stream);
+cudaError_t launch_q4_shape(const DecodeParams& p, int grid, cudaStream_t stream) {
+    if (p.dplan) return p.anc ? cudaErrorInvalidValue : launch_q4_t<D, QB, true, false>(p, grid, stream);
+    return p.anc ? launch_q4_t<D, QB, false, true>(p, grid, stream) : launch_q4_t<D, QB, false, false>(p, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_q4(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int grid, int d,
-                             cudaStream_t stream) {
+cudaError_t launch_decode_q4(const DecodeParams& p, int grid, int d, cudaStream_t stream) {
     if (p.RPB != 8 && p.RPB != 16) return cudaErrorInvalidValue;
     if (d == 128)
-        return p.RPB == 8 ? launch_q4_shape<128, 1>(p, tmK, tmV, grid, stream) : launch_q4_shape<128, 2>(p, tmK, tmV, grid, stream);
+        return p.RPB == 8 ? launch_q4_shape<128, 1>(p, grid, stream) : launch_q4_shape<128, 2>(p, grid, stream);
     if (d == 64)
-        return p.RPB == 8 ? launch_q4_shape<64, 1>(p, tmK, tmV, grid, stream) : launch_q4_shape<64, 2>(p, tmK, tmV, grid, stream);
+        return p.RPB == 8 ? launch_q4_shape<64, 1>(p, grid, stream) : launch_q4_shape<64, 2>(p, grid, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -185,34 +185,12 @@ kvc_status encode_rows_map(CUtensorMap* m, const void* base, cuuint64_t rows, cu
     return ok();
 }
 
-// The codes of a 4-bit cache: [rows, d / 2 bytes], boxes of 64 rows, with the
-// 64-byte swizzle for 64-byte rows (d = 128).
-kvc_status encode_q4_map(CUtensorMap* m, const void* base, cuuint64_t rows, int d) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(d / 2), rows};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d / 2)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(d / 2), 64};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(KVC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-    return ok();
-}
-
 // One layer's K and V as rows = B*Hkv*max_len: 64-row and 128-row boxes.
 kvc_status encode_layer_maps(kvc_cache* c, int layer) {
-    if (c->tm_ready[layer]) return ok();
+    if (c->tm_ready[layer] || c->dtype == KVC_Q4) return ok();  // (4-bit tiles come by untiled copies)
     const cuuint64_t rows = c->pg.table ? static_cast<cuuint64_t>(c->pg.num_pages) * c->Hkv * c->pg.page
                                         : static_cast<cuuint64_t>(c->B) * c->Hkv * c->max_len;
     kvc_status s;
-    if (c->dtype == KVC_Q4) {
-        if ((s = encode_q4_map(&c->tmK[layer], c->k[layer], rows, c->d))) return s;
-        if ((s = encode_q4_map(&c->tmV[layer], c->v[layer], rows, c->d))) return s;
-        c->tm_ready[layer] = 1;
-        return ok();
-    }
     const bool fp8 = c->dtype == KVC_FP8_E4M3;
     const int kt = key_tile_keys(c->d, fp8);  // the split-KV kernel's tile for this cache
     if ((s = encode_rows_map(&c->tmK[layer], c->k[layer], rows, kt, fp8, c->d))) return s;
@@ -788,7 +766,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     }
     cudaError_t e =
         c->dtype == KVC_Q4
-            ? launch_decode_q4(p, c->tmK[layer], c->tmV[layer], grid, c->d, stream)
+            ? launch_decode_q4(p, grid, c->d, stream)
             : launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], pl.mt, grid, c->dtype == KVC_FP8_E4M3, c->d, stream);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV attention launch");
     ++c->launches;
@@ -1660,7 +1638,7 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     p.pg = c->pg;
     set_decode_scales(c, layer, &p);
     p.q4 = q4_scales(c, layer);
-    e = c->dtype == KVC_Q4 ? launch_decode_q4(p, c->tmK[layer], c->tmV[layer], grid, c->d, st)
+    e = c->dtype == KVC_Q4 ? launch_decode_q4(p, grid, c->d, st)
                            : launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], 1, grid, c->dtype == KVC_FP8_E4M3, c->d, st);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV attention launch");
     ++c->launches;
