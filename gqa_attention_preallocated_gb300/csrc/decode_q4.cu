@@ -80,7 +80,7 @@ struct Q4Shape {
     static constexpr int kGroups = QB == 1 ? 3 : 2;
     static constexpr int kCW = kGroups * kTileWarps;
     static constexpr int kCT = kCW * 32;
-    static constexpr int kThreads = kCT + 32;
+    static constexpr int kThreads = kCT + 32 * kGroups;  // a producer warp a group
     static constexpr int kRows = 8 * QB;
     static constexpr int kRowB = D / 2;            // bytes of a row's codes
     static constexpr int kCodeB = kKT * kRowB;     // one tile's K (or V) codes
@@ -208,47 +208,75 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     }
     if (x0 >= x1) return;
 
-    // ------------------------------------------------------------------ producer
-    if (warp == S::kCW) {
-        if (lane == 0) {
-            Cursor<DP, kKT> cur;
-            cur.init(wp, x0);
-            int issued = 0, extent = 0, min_lim;
-            for (int x = x0, it = 0; x < x1; ++x, ++it) {
-                const int s = it % kStages;
-                const int b = cur.q / p.RB;
-                if (it == 0 || cur.j == 0) block_bounds(wp, b, cur.q - b * p.RB, extent, min_lim);
-                if (it >= kStages) {
-                    if (!ptx::mbar_wait_bounded(bar0 + 8 * (kStages + s), ((it / kStages) & 1) ^ 1, kWaitLimitNs)) {
+    // ------------------------------------------------------------------ producers
+    // One warp a group, so that the copies of consecutive tiles are issued side
+    // by side; lanes 0 .. 3 issue a tile's copies of K, V and their scale words.
+    if (warp >= S::kCW) {
+        Cursor<DP, kKT> cur;
+        cur.init(wp, x0);
+        const bool is_v = (lane & 1) != 0, is_scale = (lane & 2) != 0;
+        const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
+        const uint32_t* words = is_v ? p.q4.v : p.q4.k;
+        const uint32_t dst_off = is_scale ? 2 * S::kCodeB + (is_v ? kKT * 4 : 0) : (is_v ? S::kCodeB : 0);
+        int mine = warp - S::kCW, stage = mine, phase = 1;  // (the first round of stages is free)
+        int issued = 0;
+        bool stop = false;
+        for (int x = x0; x < x1 && !stop;) {
+            const int b = cur.q / p.RB, kvh = cur.kvh;
+            const int nseg = min(cur.nt - cur.j, x1 - x), it_end = x - x0 + nseg;
+            int extent, min_lim;
+            block_bounds(wp, b, cur.q - b * p.RB, extent, min_lim);
+            const int first = (cur.t0 + cur.j) * kKT - (x - x0) * kKT;  // + it * kKT: the tile's first key
+            // The tile's rows lie behind one another: one copy each of K, of V and
+            // of their scale words, up to the last visible key (scale words to the
+            // next multiple of 4, which the unit's stride holds).  The row of the
+            // next tile is looked up before this one's stage is waited for.
+            int row = mine < it_end ? key_row(p, b, kvh, first + mine * kKT) : 0;
+            for (; mine < it_end; mine += S::kGroups) {
+                const int n = min(kKT, extent - (first + mine * kKT));
+                const int next = mine + S::kGroups < it_end ? key_row(p, b, kvh, first + (mine + S::kGroups) * kKT) : 0;
+                const uint32_t full = bar0 + 8 * stage;
+                if (!ptx::mbar_try_wait(bar0 + 8 * (kStages + stage), phase) &&
+                    !ptx::mbar_wait_bounded(bar0 + 8 * (kStages + stage), phase, kWaitLimitNs)) {
+                    if (lane == 0) {
                         atomicExch(p.err, kDevTimeoutEmpty);
                         *abort_flag = 1;
                     }
+                    stop = true;  // (a producer is in no named barrier, so it may stop early)
                 }
-                if (*abort_flag) break;  // the producer is in no named barrier, so it may stop early
-                // The tile's rows lie behind one another: one copy each of K, of
-                // V and of their scale words, up to the last visible key (scale
-                // words to the next multiple of 4, which the unit's stride holds).
-                const int tile0 = (cur.t0 + cur.j) * kKT;
-                const int row = key_row(p, b, cur.kvh, tile0);
-                const int n = min(kKT, extent - tile0);
-                const uint32_t full = bar0 + 8 * s, sK = stage0 + s * S::kStageB, sV = sK + S::kCodeB;
-                const size_t sidx = q4::scale_index(p.q4, row), bytes = static_cast<size_t>(row) * S::kRowB;
-                const uint32_t sbytes = (n + 3) / 4 * 16;
-                ptx::mbar_arrive_expect_tx(full, 2 * (n * S::kRowB + sbytes));
-                bulk_load(sK, static_cast<const uint8_t*>(p.k_cache) + bytes, n * S::kRowB, full);
-                bulk_load(sV, static_cast<const uint8_t*>(p.v_cache) + bytes, n * S::kRowB, full);
-                bulk_load(sV + S::kCodeB, p.q4.k + sidx, sbytes, full);
-                bulk_load(sV + S::kCodeB + kKT * 4, p.q4.v + sidx, sbytes, full);
-                ++issued;
-                cur.advance(wp);
-            }
-            // Never leave the CTA with copies in flight (bounded; in a clean run
-            // these phases have completed).
-            for (int it = max(0, issued - kStages); it < issued; ++it) {
-                if (!ptx::mbar_wait_bounded(bar0 + 8 * (it % kStages), (it / kStages) & 1, kWaitLimitNs)) {
-                    atomicExch(p.err, kDevTimeoutDrain);
+                if (__any_sync(0xffffffffu, stop)) {
+                    stop = true;
                     break;
                 }
+                const uint32_t cbytes = n * S::kRowB, sbytes = (n + 3) / 4 * 16;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full, 2 * (cbytes + sbytes));
+                __syncwarp();
+                if (lane < 4)
+                    bulk_load(stage0 + stage * S::kStageB + dst_off,
+                              is_scale ? static_cast<const void*>(words + q4::scale_index(p.q4, row))
+                                       : static_cast<const void*>(src + static_cast<size_t>(row) * S::kRowB),
+                              is_scale ? sbytes : cbytes, full);
+                row = next;
+                ++issued;
+                stage += S::kGroups;
+                if (stage >= kStages) {
+                    stage -= kStages;
+                    phase ^= 1;
+                }
+            }
+            x += nseg;
+            cur.j = cur.nt - 1;
+            if (x < x1) cur.advance(wp);
+        }
+        // Never leave the CTA with copies in flight: wait (bounded) for the last
+        // phase armed on each of this warp's stages (in a clean run they have
+        // completed).
+        constexpr int kOwn = kStages / S::kGroups;  // this warp's stages
+        for (int i = max(0, issued - kOwn); i < issued; ++i) {
+            const int st = warp - S::kCW + i % kOwn * S::kGroups;
+            if (!ptx::mbar_wait_bounded(bar0 + 8 * st, (i / kOwn) & 1, kWaitLimitNs)) {
+                if (lane == 0) atomicExch(p.err, kDevTimeoutDrain);
+                break;
             }
         }
         return;
