@@ -26,8 +26,7 @@ KVC_MAX_BATCH = 1024
 
 # (name, restype, argtypes) for every entry point declared in include/kvc.h
 _VP, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-_I32P = ctypes.POINTER(ctypes.c_int32)
-_I64P = ctypes.POINTER(ctypes.c_int64)
+_I32P = _I64P = _VP  # host arrays: an address, or any ctypes array or pointer
 SIGNATURES = [
     ("kvc_create", _I, [ctypes.POINTER(_VP), _I, _I, _I, _I, _I, _I, ctypes.POINTER(_VP), ctypes.POINTER(_VP)]),
     ("kvc_create_paged", _I, [ctypes.POINTER(_VP), _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_VP),

@@ -116,12 +116,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-// Untiled copy into shared memory, counted on `bar` (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t v) {
     __half2 h;
     memcpy(&h, &v, 4);
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive_expect_tx(full, 2 * (cbytes + sbytes));
                 __syncwarp();
                 if (lane < 4)
-                    bulk_load(stage0 + stage * S::kStageB + dst_off,
+                    ptx::bulk_load(stage0 + stage * S::kStageB + dst_off,
                               is_scale ? static_cast<const void*>(words + q4::scale_index(p.q4, row))
                                        : static_cast<const void*>(src + static_cast<size_t>(row) * S::kRowB),
                               is_scale ? sbytes : cbytes, full);

@@ -84,7 +84,10 @@ namespace {
 // against 1,670).
 constexpr int kTcMinRows = 12;
 constexpr int kTcMinRowsFp8 = 32;
-int tc_min_rows(const kvc_cache* c) { return c->dtype == KVC_FP8_E4M3 ? kTcMinRowsFp8 : kTcMinRows; }
+constexpr int kTcMinRowsQ4 = 16;
+int tc_min_rows(const kvc_cache* c) {
+    return c->dtype == KVC_Q4 ? kTcMinRowsQ4 : c->dtype == KVC_FP8_E4M3 ? kTcMinRowsFp8 : kTcMinRows;
+}
 // Caches served by the generic kernel (attn_f32.cu) only: fp32 storage, and
 // bf16 or FP8 storage whose head dimension has no TMA kernel (the split-KV
 // kernel takes d = 128, and d = 64 for bf16; the tensor-core kernel d = 128).
@@ -92,8 +95,8 @@ bool generic_path(const kvc_cache* c) {
     return c->dtype == KVC_F32 ||
            !(c->d == kHeadDimBf16 || (c->d == kHeadDimSmall && (c->dtype == KVC_BF16 || c->dtype == KVC_Q4)));
 }
-// Head dimension the tensor-core kernel is built for.
-bool tc_capable(const kvc_cache* c) { return !generic_path(c) && c->d == kHeadDimBf16 && c->dtype != KVC_Q4; }
+// Head dimensions the tensor-core kernel is built for: 128, and 64 for 4-bit caches.
+bool tc_capable(const kvc_cache* c) { return !generic_path(c) && (c->d == kHeadDimBf16 || c->dtype == KVC_Q4); }
 // Keys per tile of the split-KV kernel that serves this cache.
 int split_tile_keys(const kvc_cache* c) {
     return c->dtype == KVC_Q4 ? kQ4KeyTile : key_tile_keys(c->d, c->dtype == KVC_FP8_E4M3);
@@ -304,7 +307,7 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
             // The tensor-core kernel: up to two partial slots (2 row tiles x
             // 128 rows x (d + 4) floats) per SM share boundary.
             const size_t prefill = static_cast<size_t>(2) * std::min(num_ctas, kMaxCtas) * 2 * 128 *
-                                   (kHeadDimBf16 + 4) * sizeof(float);
+                                   (c->d + 4) * sizeof(float);
             pl->ws_partials = std::max(pl->ws_partials, prefill);
             if (c->max_len <= kTcMaxLen) pl->ws_min = pl->ws_err + pl->ws_plan;
         }
@@ -510,6 +513,10 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 pp.kscale[h] = c->kscale[static_cast<size_t>(layer) * c->Hkv + h];
                 pp.vscale[h] = c->vscale[static_cast<size_t>(layer) * c->Hkv + h];
             }
+        pp.d = c->d;
+        pp.q4 = q4_scales(c, layer);
+        pp.k_cache = static_cast<const uint8_t*>(c->k[layer]);
+        pp.v_cache = static_cast<const uint8_t*>(c->v[layer]);
         pp.ntb = pp.mode == 0 ? (pl.T + 127) / 128 : 1;
         pp.npair = pp.mode == 0 ? (pl.G + 1) / 2 : (pl.R + 255) / 256;
         pp.window = c->window;
@@ -543,7 +550,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                     }
                 }
         }
-        const size_t slot_bytes = static_cast<size_t>(2) * 128 * (kHeadDimBf16 + 4) * sizeof(float);
+        const size_t slot_bytes = static_cast<size_t>(2) * 128 * (c->d + 4) * sizeof(float);
         const long long slot_room =
             std::min<long long>(kMaxPrefillSlots, static_cast<long long>((ws_bytes - pl.ws_err - pl.ws_plan) / slot_bytes));
         const int nsm = std::max(1, c->num_sms);
@@ -552,7 +559,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         bool launched = false;
         if (!items.empty()) {
             CUtensorMap tmQ;
-            if ((s = encode_rows_map(&tmQ, q, static_cast<cuuint64_t>(c->B) * pl.Hq * pl.T, 128))) return s;
+            if ((s = encode_rows_map(&tmQ, q, static_cast<cuuint64_t>(c->B) * pl.Hq * pl.T, 128, false, c->d))) return s;
             if (ws != c->last_ws) {
                 cudaError_t e = cudaMemsetAsync(ws, 0, pl.ws_err, stream);
                 if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");

@@ -295,6 +295,9 @@ struct PrefillParams {
     int window, ring;  // sliding window (0 = none) and ring storage, as in DecodeParams
     Paging pg;
     float scale_log2;
+    int d;             // 128, or 64 for a 4-bit cache
+    Q4Scales q4;       // 4-bit cache: the rows' scale words (k null otherwise) and their codes
+    const uint8_t *k_cache, *v_cache;
     int prior[kMaxBatch];
     int n_new[kMaxBatch];
     // One CTA per piece, in launch order.
@@ -305,7 +308,6 @@ struct PrefillParams {
     uint32_t piece_aux[kMaxPrefillPieces];
 };
 
-size_t prefill_smem_bytes();
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                               const CUtensorMap& tmV, cudaStream_t stream);
 

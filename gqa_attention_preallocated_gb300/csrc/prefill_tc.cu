@@ -25,7 +25,19 @@
 // to f16 once), and the MMAs run kind::f16 on f16 operands; the K scale folds
 // into the softmax scale and the V scale into the output normalisation.
 //
-// Warp roles (12 warps):
+// 4-bit caches (KVC_Q4; also d = 64): a tile's codes and scale words arrive by
+// untiled copies in a ring of three raw slots, K and V in turn; two warps
+// convert K and two more V into the bf16 tiles the MMAs read.  A value is
+// s * (c - z), rounded once to bf16: c - z is exact in bf16 and one product
+// rounds it, so the MMAs see what kvc_read gives.  (Folding the step into the
+// softmax instead, as the split-KV kernel does, would cost a multiply a score
+// and a weight, 256 rows x 128 keys a tile, where the conversion's is one a
+// value, 128 x 128, on warps that are otherwise idle; and f16 operands would
+// need a range check.)  A V row whose step is NaN is written as zeros and its K
+// row as NaN: the score carries the NaN to the queries that see the key, and
+// the others' zero weights meet a zero.
+//
+// Warp roles (12 warps, 14 for 4-bit caches):
 //   warp 0      TMA producer: Q tiles once, then K and V tiles (128 keys) into
 //               two-stage rings guarded by mbarriers.
 //   warp 1      MMA issuer (one lane): S_i = Q_i K^T into TMEM, then, once the
@@ -33,6 +45,7 @@
 //               P_i as the TMEM A operand.  Issue order S0(j), S1(j), PV0(j),
 //               S0(j+1), PV1(j), S1(j+1), ... keeps the tensor core busy while
 //               each softmax warpgroup works on the other head's tile.
+//   warps 2, 3  FP8: converters; 4-bit: converters of K (12, 13: of V)
 //   warps 4-7   softmax of row tile 0 (mode 2: even key tiles), one thread per query row
 //   warps 8-11  softmax of row tile 1 (mode 2: odd key tiles)
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).
@@ -60,15 +73,19 @@
 
 #include "kvc_internal.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 
 namespace kvc {
 
 namespace {
 
-constexpr int kThreadsPF = 384;  // 4 warps (producer, MMA issuer, 2 converters / idle) + 8 softmax warps
-constexpr int kD = 128;
+// Storage of the cache.
+enum Fmt : int { kFmtBf16 = 0, kFmtFp8 = 1, kFmtQ4 = 2 };
+// 4 warps (producer, MMA issuer, 2 converters / idle) + 8 softmax warps; with
+// 4-bit storage two more converters.
+__host__ __device__ constexpr int threads_pf(int fmt) { return fmt == kFmtQ4 ? 448 : 384; }
 constexpr int kBoxBytes = 128 * 128;           // 128 rows x 64 columns x 2 B (one swizzled box)
-constexpr int kTile128 = 2 * kBoxBytes;         // 128 rows x 128 columns
+constexpr int kTile128 = 2 * kBoxBytes;         // 128 rows x 128 columns (d = 64 uses the first box)
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescaleThreshold = 8.0f;       // log2 of the largest factor kept unrescaled
 
@@ -80,15 +97,23 @@ constexpr int kOffBar = 6 * kTile128;
 // A split piece's epilogue stages head i's 128 x (d + 4) float partial block
 // at kOffQ + i * kSplitStageBytes: Q, the K stages and the first 4 KB of V
 // stage 0, all idle once that head's last PV product has landed.
-constexpr int kSplitStageBytes = 128 * (kD + 4) * 4;
+constexpr int kSplitStageBytes = 128 * (128 + 4) * 4;
 static_assert(2 * kSplitStageBytes <= kOffBar, "split staging fits below the barriers");
+// 4-bit caches: raw slots of one K or V tile (128 rows of d / 2 bytes, then K's
+// and V's scale words) behind the barriers.
+constexpr int kOffRaw = kOffBar + 256;
+constexpr int kRawScaleK = 128 * 64, kRawScaleV = kRawScaleK + 512, kRawBytes = kRawScaleV + 512;
+constexpr int kRawSlots = 3;
 // barrier indices
 // (FP8 caches: TMA completes the *Raw barriers, the converter warps then arm
 // Q / KFull / VFull once the tiles are f16)
 constexpr int kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9, kBarP = 11,
-              kBarO = 13, kBarQRaw = 15, kBarKRaw = 16, kBarVRaw = 18, kNumBars = 20;
+              kBarO = 13, kBarQRaw = 15, kBarKRaw = 16, kBarVRaw = 18;
+constexpr int kBarRawFull = 20, kBarRawEmpty = 23, kNumBars = 26;  // 4-bit caches' raw slots
 constexpr int kConvThreads = 64;  // warps 2 and 3
 constexpr size_t kSmemPF = 1024 + kOffBar + 256;
+constexpr size_t kSmemQ4 = kSmemPF + kRawSlots * kRawBytes;
+static_assert(kNumBars * 8 + 24 <= 256 && kSmemQ4 <= 232448, "shared memory map");
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
     // tcgen05 shared-memory matrix descriptor: start >> 4, leading / stride byte
@@ -97,11 +122,68 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, bf16 (or f16) A and B, M = N = 128.
-__device__ __forceinline__ uint32_t instr_desc(bool b_mn_major, bool f16 = false) {
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 (or f16) A and B, M = 128.
+__device__ __forceinline__ uint32_t instr_desc(bool b_mn_major, bool f16, int n) {
     const uint32_t ab = f16 ? 0u : ((1u << 7) | (1u << 10));  // A and B format: 0 = f16, 1 = bf16
-    return (1u << 4) | ab | (static_cast<uint32_t>(b_mn_major) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | ab | (static_cast<uint32_t>(b_mn_major) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
+
+// 4-bit caches: rows r and r + 64 of a raw slot (d / 2 bytes a row) into the
+// bf16 tile the MMAs read (64-column boxes, 128-byte swizzle).  A thread owns
+// whole rows and takes its 16-byte pieces in an order that starts at r / 2, so
+// that eight neighbouring rows read eight different bank groups (their strides
+// are 64 bytes) and write eight too.
+template <int kDim>
+struct RawRows {
+    static constexpr int kPieces = kDim / 32;  // 16-byte pieces of a row: 32 codes
+    uint4 w[2][kPieces];
+    uint32_t own[2], other[2];  // the row's scale word, and the other tensor's
+    __device__ __forceinline__ void load(const uint8_t* raw, int ct, bool is_v) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = ct + 64 * h;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                w[h][i] = *reinterpret_cast<const uint4*>(raw + r * (kDim / 2) + ((i + (r >> 1)) % kPieces) * 16);
+            const uint32_t k = *reinterpret_cast<const uint32_t*>(raw + kRawScaleK + r * 4);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(raw + kRawScaleV + r * 4);
+            own[h] = is_v ? v : k;
+            other[h] = is_v ? k : v;
+        }
+    }
+    __device__ __forceinline__ void convert(uint8_t* tile, int ct, bool is_v) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = ct + 64 * h;
+            auto is_nan = [](uint32_t word) { return (word & 0x7FFF0000u) >= 0x7F800000u; };
+            uint32_t s = __byte_perm(own[h], 0, 0x3232);  // the step in both halves
+            if (is_v) {
+                if (is_nan(own[h])) s = 0u;
+            } else if (is_nan(other[h])) {
+                s = 0x7FC07FC0u;
+            }
+            const uint32_t z = 0x43004300u + (own[h] & 0xFFu) * 0x00010001u;  // 128 + z, twice
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int piece = (i + (r >> 1)) % kPieces;
+                const uint32_t u[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // word k: columns 32 piece + 8k .. + 7
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t c = ((u[k] >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + c, twice
+                        o[e] = ptx::mul_bf16x2(ptx::sub_bf16x2(c, z), s);
+                    }
+                    const int cc = piece * 4 + k;  // 16-byte chunk of the row
+                    *reinterpret_cast<uint4*>(tile + (cc >> 3) * kBoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    }
+};
+
 
 // FP8 caches: one 128-key tile of E4M3 codes (128 rows x 128 bytes, 128-byte
 // swizzle) sits in the second half of a stage; convert it in place to the f16
@@ -291,6 +373,7 @@ __device__ __forceinline__ Piece decode_piece(const PrefillParams& p, int idx) {
 // piece's block in with cp.async, all of it in flight at once.  tS: this
 // head's S columns, idle by now, hold the running sum of O when a block has
 // more than two pieces.
+template <int kD>
 __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t tS, uint32_t tO, int i, int r, bool valid,
                                             float m_ref, float l, int slot, int kidx, int npc, __nv_bfloat16* dst,
                                             volatile int* merge_flag, float out_scale, float* stage) {
@@ -304,7 +387,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
     // staging block (the packed mode's exchange of the odd-tile state).
     ptx::named_barrier_sync(1 + i, 128);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < kD / 32; ++c) {
         uint32_t w[32];
         tmem_ld32(tO + c * 32, w);
         tmem_ld_wait();
@@ -380,7 +463,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
         // its staged block.
         const float w_own = weight(kidx), w_oth = weight(1 - kidx);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kD / 32; ++c) {
             uint32_t w[32];
             tmem_ld32(tO + c * 32, w);
             tmem_ld_wait();
@@ -406,7 +489,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
             if (!own) stage_piece(k);
             const float wk = weight(k);
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kD / 32; ++c) {
                 float ok[32], acc[32];
                 uint32_t w[32];
                 if (own) {
@@ -448,11 +531,14 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
 // one the window code is compiled out.  kAlt: mode 2 (one packed row tile,
 // alternate key tiles per TMEM buffer); modes 0 and 1 otherwise.  kF8: the
 // cache holds E4M3 codes (converted to f16 in shared memory by warps 2 and 3;
-// the MMAs run on f16 with the queries converted too).
-template <bool kWin, bool kAlt, bool kF8>
-__global__ void __launch_bounds__(kThreadsPF, 1)
+// the MMAs run on f16 with the queries converted too; 4-bit rows are converted
+// to bf16 by four warps.  kD: the head dimension (64 with 4-bit storage only).
+template <bool kWin, bool kAlt, int kFmt, int kD>
+__global__ void __launch_bounds__(threads_pf(kFmt), 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    constexpr bool kF8 = kFmt == kFmtFp8, kQ4 = kFmt == kFmtQ4;
+    constexpr int kThreadsPF = threads_pf(kFmt), kBoxes = kD / 64;  // 64-column boxes of a row tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = ptx::smem_addr(smem);
@@ -465,8 +551,12 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        const int ready = kF8 ? 2 : 1;  // FP8: both converter warps arrive; else the TMA's arrive
-        ptx::mbar_init(bar(kBarQ), ready);
+        const int ready = kF8 || kQ4 ? 2 : 1;  // both converter warps arrive; else the TMA's arrive
+        ptx::mbar_init(bar(kBarQ), kF8 ? 2 : 1);
+        for (int s = 0; s < kRawSlots && kQ4; ++s) {
+            ptx::mbar_init(bar(kBarRawFull + s), 1);
+            ptx::mbar_init(bar(kBarRawEmpty + s), 2);
+        }
         ptx::mbar_init(bar(kBarQRaw), 1);
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(bar(kBarKFull + s), ready);
@@ -484,8 +574,10 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
     }
     if (warp == 0 && lane == 0) {
         ptx::tma_prefetch_desc(&tmQ);
-        ptx::tma_prefetch_desc(&tmK);
-        ptx::tma_prefetch_desc(&tmV);
+        if (!kQ4) {
+            ptx::tma_prefetch_desc(&tmK);
+            ptx::tma_prefetch_desc(&tmV);
+        }
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -535,15 +627,38 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             const int qbar = kF8 ? kBarQRaw : kBarQ;
-            ptx::mbar_arrive_expect_tx(bar(qbar), nh * kTile128);
+            ptx::mbar_arrive_expect_tx(bar(qbar), nh * kBoxes * kBoxBytes);
             for (int i = 0; i < nh; ++i) {
                 // mode 0: 128 positions of head h0 + i; modes 1, 2: 128 packed rows
                 const int qrow = (p.mode == 0) ? ((b * p.Hq) + h0 + i) * p.T + t0
                                                : (b * p.Hq + h0) * p.T + pc.pr0 + i * 128;
-                for (int hf = 0; hf < 2; ++hf)
+                for (int hf = 0; hf < kBoxes; ++hf)
                     ptx::tma_load_2d(sbase + kOffQ + i * kTile128 + hf * kBoxBytes, &tmQ, hf * 64, qrow, bar(qbar));
             }
-            for (int j = 0; j < nkt && !*abort_flag; ++j) {
+            if constexpr (kQ4) {
+                // Items K0, V0, K1, V1, ... take the raw slots in turn: the tile's
+                // rows up to the last visible key, and their scale words (of both
+                // tensors with K).
+                for (int n = 0; n < 2 * nkt && !*abort_flag; ++n) {
+                    const int key0 = (kt0 + (n >> 1)) * 128, sl = n % kRawSlots;
+                    const bool is_v = (n & 1) != 0;
+                    const int row = slot_row(kt0 + (n >> 1)), rows = min(128, kmax - key0 + 1);
+                    if (n >= kRawSlots &&
+                        !ptx::mbar_wait_bounded(bar(kBarRawEmpty + sl), ((n / kRawSlots) & 1) ^ 1, kWaitNs)) {
+                        atomicExch(p.err, kDevTimeoutEmpty);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    const size_t bytes = static_cast<size_t>(row) * (kD / 2), sidx = q4::scale_index(p.q4, row);
+                    const uint32_t dst = sbase + kOffRaw + sl * kRawBytes, full = bar(kBarRawFull + sl);
+                    const uint32_t cb = rows * (kD / 2), sb = (rows + 3) / 4 * 16;
+                    ptx::mbar_arrive_expect_tx(full, cb + (is_v ? 1 : 2) * sb);
+                    ptx::bulk_load(dst, (is_v ? p.v_cache : p.k_cache) + bytes, cb, full);
+                    ptx::bulk_load(dst + kRawScaleV, p.q4.v + sidx, sb, full);
+                    if (!is_v) ptx::bulk_load(dst + kRawScaleK, p.q4.k + sidx, sb, full);
+                }
+            }
+            for (int j = 0; j < nkt && !kQ4 && !*abort_flag; ++j) {
                 const int s = j & 1;
                 const int row = slot_row(kt0 + j);
                 if (j >= 2 && !ptx::mbar_wait_bounded(bar(kBarKEmpty + s), ((j >> 1) & 1) ^ 1, kWaitNs)) {
@@ -602,9 +717,33 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
             convert_e4m3_tile(smem + kOffV + s * kTile128, ct);
             ready(kBarVFull + s);
         }
+    } else if (kQ4 && (warp == 2 || warp == 3 || warp >= 12)) {
+        // ------------------------------------------------------------ 4-bit -> bf16 converters
+        const bool is_v = warp >= 12;
+        const int ct = (is_v ? tid - 384 : tid - 64);
+        auto wait_for = [&](int b_idx, int parity) {
+            if (!ptx::mbar_wait_bounded(bar(b_idx), parity, *abort_flag ? 0ull : kWaitNs)) {
+                atomicExch(p.err, kDevTimeoutFull);
+                *abort_flag = 1;
+            }
+        };
+        const int tile0 = is_v ? kOffV : kOffK, bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
+        for (int j = 0; j < nkt; ++j) {
+            const int s = j & 1, n = 2 * j + (is_v ? 1 : 0), sl = n % kRawSlots;
+            RawRows<kD> rows;
+            wait_for(kBarRawFull + sl, (n / kRawSlots) & 1);
+            rows.load(smem + kOffRaw + sl * kRawBytes, ct, is_v);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));
+            if (j >= 2) wait_for(bar_empty + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
+            rows.convert(smem + tile0 + s * kTile128, ct, is_v);
+            ptx::fence_proxy_async_smem();  // generic writes -> visible to the tensor core
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(bar_full + s));
+        }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t id_qk = instr_desc(false, kF8), id_pv = instr_desc(true, kF8);
+        const uint32_t id_qk = instr_desc(false, kF8, 128), id_pv = instr_desc(true, kF8, kD);
         auto wait = [&](int b_idx, int parity) {
             if (!ptx::mbar_wait_bounded(bar(b_idx), parity, *abort_flag ? 0ull : kWaitNs)) {
                 atomicExch(p.err, kDevTimeoutFull);
@@ -614,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
         auto issue_s = [&](int i, int j, int qi) {  // S_i = Q_qi K_j^T
             const uint32_t qa = sbase + kOffQ + qi * kTile128, ka = sbase + kOffK + (j & 1) * kTile128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kD / 16; ++k) {
                 const uint32_t off = (k >> 2) * kBoxBytes + (k & 3) * 32;
                 mma_ss(tmem + i * 128, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), id_qk, k > 0);
             }
@@ -660,7 +799,7 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
                 uint8_t* vb = smem + kOffV + s * kTile128;
                 const int per_hi = (128 - vr0) * 8, per_lo = vr1 * 8;
 #pragma unroll 1
-                for (int idx = lane; idx < 2 * (per_hi + per_lo); idx += 32) {
+                for (int idx = lane; idx < kBoxes * (per_hi + per_lo); idx += 32) {
                     const int hf = idx / (per_hi + per_lo), rem = idx - hf * (per_hi + per_lo);
                     const int row = rem < per_lo ? (rem >> 3) : vr0 + ((rem - per_lo) >> 3);
                     *reinterpret_cast<uint4*>(vb + hf * kBoxBytes + row * 128 + (rem & 7) * 16) =
@@ -702,7 +841,7 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
             }
             __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ softmax (one thread per query row)
         const int i = (warp - 4) >> 2;  // S/O buffer: row tile of the pair, or in mode 2 key-tile parity
         const int r = tid & 127;        // row in the block = TMEM lane
@@ -775,7 +914,7 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
                         }
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 2; ++c) {
+                        for (int c = 0; c < kD / 64; ++c) {
                             tmem_ld64(tO + c * 64, v);
                             tmem_ld_wait();
                             uint32_t w[32];
@@ -853,7 +992,7 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
                     const float f0 = (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - Mu);
                     const float f1 = (m1 == -INFINITY) ? 0.f : ptx::ex2(m1 - Mu);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kD / 32; ++c) {
                         uint32_t w0[32], w1[32];
                         tmem_ld32(tO + c * 32, w0);
                         tmem_ld32(tO + 128 + c * 32, w1);
@@ -875,13 +1014,13 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
             if (alt && i == 1) {
                 // state handed to warpgroup 0
             } else if (pc.slot != kPrefillNoSlot) {
-                split_epilogue(p.partials, p.err, tS, tO, i, r, valid, m_ref, l, pc.slot, pc.kidx, pc.npc, dst, merge_flag,
+                split_epilogue<kD>(p.partials, p.err, tS, tO, i, r, valid, m_ref, l, pc.slot, pc.kidx, pc.npc, dst, merge_flag,
                                kF8 ? p.vscale[kvh] : 1.f,
                                reinterpret_cast<float*>(smem + kOffQ + i * kSplitStageBytes));
             } else {
             const float inv = (valid && l > 0.f) ? (kF8 ? p.vscale[kvh] : 1.f) / l : 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < kD / 32; ++c) {
                 uint32_t w[32];
                 tmem_ld32(tO + c * 32, w);
                 tmem_ld_wait();
@@ -911,45 +1050,48 @@ __global__ void __launch_bounds__(kThreadsPF, 1)
 
 }  // namespace
 
-size_t prefill_smem_bytes() { return kSmemPF; }
+namespace {
 
-cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                              const CUtensorMap& tmV, cudaStream_t stream) {
+template <int kFmt, int kD>
+cudaError_t launch_fmt(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                       cudaStream_t stream) {
+    using Kernel = void (*)(PrefillParams, CUtensorMap, CUtensorMap, CUtensorMap);
+    static const Kernel kernels[2][2] = {{prefill_tc_kernel<false, false, kFmt, kD>, prefill_tc_kernel<false, true, kFmt, kD>},
+                                         {prefill_tc_kernel<true, false, kFmt, kD>, prefill_tc_kernel<true, true, kFmt, kD>}};
+    constexpr size_t smem = kFmt == kFmtQ4 ? kSmemQ4 : kSmemPF;
     static bool attr_set = false;
     if (!attr_set) {
-        for (auto* k : {prefill_tc_kernel<false, false, false>, prefill_tc_kernel<true, false, false>,
-                        prefill_tc_kernel<false, true, false>, prefill_tc_kernel<true, true, false>,
-                        prefill_tc_kernel<false, false, true>, prefill_tc_kernel<true, false, true>,
-                        prefill_tc_kernel<false, true, true>, prefill_tc_kernel<true, true, true>}) {
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(kSmemPF));
-            if (e != cudaSuccess) return e;
-        }
+        for (auto& row : kernels)
+            for (Kernel k : row) {
+                cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                if (e != cudaSuccess) return e;
+            }
         attr_set = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_pieces);
-    cfg.blockDim = dim3(kThreadsPF);
-    cfg.dynamicSmemBytes = kSmemPF;
+    cfg.blockDim = dim3(threads_pf(kFmt));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool win = p.window > 0 || p.ring;
-    const bool alt = p.mode == 2;
-    using Kernel = void (*)(PrefillParams, CUtensorMap, CUtensorMap, CUtensorMap);
-    Kernel k;
-    if (p.fp8)
-        k = win ? (alt ? prefill_tc_kernel<true, true, true> : prefill_tc_kernel<true, false, true>)
-                : (alt ? prefill_tc_kernel<false, true, true> : prefill_tc_kernel<false, false, true>);
-    else
-        k = win ? (alt ? prefill_tc_kernel<true, true, false> : prefill_tc_kernel<true, false, false>)
-                : (alt ? prefill_tc_kernel<false, true, false> : prefill_tc_kernel<false, false, false>);
+    const Kernel k = kernels[p.window > 0 || p.ring][p.mode == 2];
     cudaError_t e = cudaLaunchKernelEx(&cfg, k, p, tmQ, tmK, tmV);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                              const CUtensorMap& tmV, cudaStream_t stream) {
+    if (p.q4.k) {  // (a 4-bit cache has no tensor maps for K and V)
+        return p.d == 64 ? launch_fmt<kFmtQ4, 64>(p, tmQ, tmQ, tmQ, stream) : launch_fmt<kFmtQ4, 128>(p, tmQ, tmQ, tmQ, stream);
+    }
+    return p.fp8 ? launch_fmt<kFmtFp8, 128>(p, tmQ, tmK, tmV, stream) : launch_fmt<kFmtBf16, 128>(p, tmQ, tmK, tmV, stream);
 }
 
 }  // namespace kvc
