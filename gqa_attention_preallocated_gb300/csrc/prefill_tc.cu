@@ -26,8 +26,11 @@
 // into the softmax scale and the V scale into the output normalisation.
 //
 // 4-bit caches (KVC_Q4; also d = 64): a tile's codes and scale words arrive by
-// untiled copies in a ring of three raw slots, K and V in turn; two warps
-// convert K and two more V into the bf16 tiles the MMAs read.  A value is
+// untiled copies in raw slots, two for K and one for V (its converters hold
+// the next tile in registers while they wait for its stage); two warps convert
+// K and two more V into the bf16 tiles the MMAs read.  K and V have slots of
+// their own because an mbarrier's parity cannot tell phases two apart: a slot
+// that both used would let the converters that run ahead read it early.  A value is
 // s * (c - z), rounded once to bf16: c - z is exact in bf16 and one product
 // rounds it, so the MMAs see what kvc_read gives.  (Folding the step into the
 // softmax instead, as the split-KV kernel does, would cost a multiply a score
@@ -103,7 +106,7 @@ static_assert(2 * kSplitStageBytes <= kOffBar, "split staging fits below the bar
 // and V's scale words) behind the barriers.
 constexpr int kOffRaw = kOffBar + 256;
 constexpr int kRawScaleK = 128 * 64, kRawScaleV = kRawScaleK + 512, kRawBytes = kRawScaleV + 512;
-constexpr int kRawSlots = 3;
+constexpr int kRawSlots = 3;  // K of even tiles, K of odd tiles, V
 // barrier indices
 // (FP8 caches: TMA completes the *Raw barriers, the converter warps then arm
 // Q / KFull / VFull once the tiles are f16)
@@ -636,15 +639,15 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                     ptx::tma_load_2d(sbase + kOffQ + i * kTile128 + hf * kBoxBytes, &tmQ, hf * 64, qrow, bar(qbar));
             }
             if constexpr (kQ4) {
-                // Items K0, V0, K1, V1, ... take the raw slots in turn: the tile's
-                // rows up to the last visible key, and their scale words (of both
-                // tensors with K).
-                for (int n = 0; n < 2 * nkt && !*abort_flag; ++n) {
-                    const int key0 = (kt0 + (n >> 1)) * 128, sl = n % kRawSlots;
+                // K, then V of each tile: its rows up to the last visible key and
+                // their scale words (of both tensors with K).
+                int issued = 0;
+                for (int n = 0; n < 2 * nkt && !*abort_flag; ++n, ++issued) {
+                    const int j = n >> 1, key0 = (kt0 + j) * 128;
                     const bool is_v = (n & 1) != 0;
-                    const int row = slot_row(kt0 + (n >> 1)), rows = min(128, kmax - key0 + 1);
-                    if (n >= kRawSlots &&
-                        !ptx::mbar_wait_bounded(bar(kBarRawEmpty + sl), ((n / kRawSlots) & 1) ^ 1, kWaitNs)) {
+                    const int sl = is_v ? 2 : (j & 1), turn = is_v ? j : j >> 1;  // the slot and which use of it this is
+                    const int row = slot_row(kt0 + j), rows = min(128, kmax - key0 + 1);
+                    if (turn > 0 && !ptx::mbar_wait_bounded(bar(kBarRawEmpty + sl), (turn & 1) ^ 1, kWaitNs)) {
                         atomicExch(p.err, kDevTimeoutEmpty);
                         *abort_flag = 1;
                         break;
@@ -656,6 +659,16 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                     ptx::bulk_load(dst, (is_v ? p.v_cache : p.k_cache) + bytes, cb, full);
                     ptx::bulk_load(dst + kRawScaleV, p.q4.v + sidx, sb, full);
                     if (!is_v) ptx::bulk_load(dst + kRawScaleK, p.q4.k + sidx, sb, full);
+                }
+                // Never leave the CTA with copies in flight: the last use of each
+                // slot has landed (bounded; in a clean run the converters saw to it).
+                for (int n = max(0, issued - 4); n < issued; ++n) {
+                    const int j = n >> 1, sl = (n & 1) ? 2 : (j & 1), turn = (n & 1) ? j : j >> 1;
+                    if (n + ((n & 1) ? 2 : 4) < issued) continue;  // a later use follows
+                    if (!ptx::mbar_wait_bounded(bar(kBarRawFull + sl), turn & 1, kWaitNs)) {
+                        atomicExch(p.err, kDevTimeoutDrain);
+                        break;
+                    }
                 }
             }
             for (int j = 0; j < nkt && !kQ4 && !*abort_flag; ++j) {
@@ -729,9 +742,9 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
         };
         const int tile0 = is_v ? kOffV : kOffK, bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
         for (int j = 0; j < nkt; ++j) {
-            const int s = j & 1, n = 2 * j + (is_v ? 1 : 0), sl = n % kRawSlots;
+            const int s = j & 1, sl = is_v ? 2 : s, turn = is_v ? j : j >> 1;
             RawRows<kD> rows;
-            wait_for(kBarRawFull + sl, (n / kRawSlots) & 1);
+            wait_for(kBarRawFull + sl, turn & 1);
             rows.load(smem + kOffRaw + sl * kRawBytes, ct, is_v);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));

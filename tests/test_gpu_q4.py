@@ -151,6 +151,7 @@ class Pair:
         else:
             out = self.c.append_attention(self.layer, q.cuda(), k.cuda(), v.cuda(), n_new)
         self.note(k, v, n_new)
+        self.last_q = q.cuda()
         assert np.array_equal(self.c.lens(self.layer), self.lens)
         self.check_out(out, q, n_new, T, parents, tag=(self.calls, T, G))
         return out
@@ -486,6 +487,22 @@ def test_longer_decode(d, B, Hkv, G, L):
     a = p.c.gqa_attention(0, q, np.ones(B))
     for _ in range(3):  # the same bits every time
         assert torch.equal(a, p.c.gqa_attention(0, q, np.ones(B)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,G,window", [(200, 3, 0), (40, 4, 0), (9, 4, 0), (150, 4, 3000)])
+def test_long_prefill(d, T, G, window):
+    """Many key tiles a block, blocks cut into pieces, ragged priors and chunks: the converters' slots turn over often."""
+    p = Pair(3, 2, d, 8300, window=window, seed=T + G)
+    n = [8011, 3000, 5557]
+    q, k, v = p.inputs(n, 8011, 1)
+    p.c.append(0, k.cuda(), v.cuda(), n)
+    p.note(k, v, n)
+    for n_new in ([T, T - 1, T // 2], [1, T, T]):
+        out = p.step(n_new, G, T=T)
+        for _ in range(3):
+            again = p.c.gqa_attention(0, p.last_q, n_new)
+            assert torch.equal(out, again)
 
 
 def test_streams_and_two_caches():
