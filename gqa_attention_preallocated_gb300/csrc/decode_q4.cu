@@ -446,18 +446,11 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                         }
                 }
             }
+            // (Each thread compares its own keys' maxima; they are joined only when
+            // some row's reference has to move.)
             bool move = ve > vexp;
 #pragma unroll
-            for (int nb = 0; nb < QB; ++nb)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float t = mx[nb][c];
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    mx[nb][c] = t;
-                    move |= t > m[nb][c] + kLazyRescale;
-                }
+            for (int nb = 0; nb < QB; ++nb) move |= mx[nb][0] > m[nb][0] + kLazyRescale || mx[nb][1] > m[nb][1] + kLazyRescale;
             if (__any_sync(0xffffffffu, move)) {
                 // Move the references; O, l and the zero points' sum follow.
                 ve = max(vexp, __reduce_max_sync(0xffffffffu, ve));
@@ -470,6 +463,8 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     float f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx[nb][c] = fmaxf(mx[nb][c], __shfl_xor_sync(0xffffffffu, mx[nb][c], d));
                         const bool mv = mx[nb][c] > m[nb][c] + kLazyRescale;
                         const float al = !mv ? 1.f : (m[nb][c] == -INFINITY) ? 0.f : ptx::ex2(m[nb][c] - mx[nb][c]);
                         if (mv) {
@@ -570,14 +565,10 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                                          ((static_cast<size_t>(b) * p.Hkv + kvh) * p.Tn + (pos - prior)) * (D * 2);
                     const uint4 val = live ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t w[4] = {val.x, val.y, val.z, val.w};
-                    float a, z;
-                    q4::range8(w, a, z);
+                    uint32_t range = q4::range8(w);
 #pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) {
-                        a = fminf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                        z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, d));
-                    }
-                    const q4::RowScale sc = q4::row_scale(a, z);
+                    for (int d = 8; d > 0; d >>= 1) range = q4::max2(range, __shfl_xor_sync(0xffffffffu, range, d));
+                    const q4::RowScale sc = q4::row_scale(range);
                     const uint32_t code = q4::encode8(w, sc);
                     bool bad = false;
                     const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, kvh, pos, &bad);

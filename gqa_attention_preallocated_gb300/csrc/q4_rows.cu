@@ -26,90 +26,142 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Rows of a thread: with long chunks four, whose loads are in flight together
+// (a prompt of 4 x 8192 tokens, d = 128: 1 and 4 rows measured, see the table
+// of operators); with few rows one, for more blocks.
+constexpr int kManyRows = 4;
+
 // LANES: lanes a row (a power of two, d / 8 or more of them: the others idle).
-template <int LANES>
+template <int LANES, int ROWS>
 __global__ void __launch_bounds__(kThreads) append_q4_kernel(const __grid_constant__ AppendParams p) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
+    constexpr int kStep = kThreads / LANES;  // rows a block takes side by side
     const int b = blockIdx.z, h = blockIdx.y >> 1;
     const bool is_v = (blockIdx.y & 1) != 0;
     const int n = p.n_new[b];
     const int sub = threadIdx.x % LANES;
-    const int t = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    if (blockIdx.x * (kThreads / LANES) >= n) return;
+    const int t0 = blockIdx.x * (kStep * ROWS) + threadIdx.x / LANES;
+    if (blockIdx.x * (kStep * ROWS) >= n) return;
     const int vecs = p.row_bytes / 16;  // 16-byte vectors of a bf16 row
-    const bool live = t < n && sub < vecs;
     const size_t unit = static_cast<size_t>(b) * p.Hkv + h;
-    const uint8_t* src = (is_v ? p.v_new : p.k_new) + unit * p.T * p.row_bytes;
-    uint4 val = make_uint4(0u, 0u, 0u, 0u);
-    if (live) val = __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(t) * p.row_bytes) + sub);
-    const uint32_t w[4] = {val.x, val.y, val.z, val.w};
-    float lo, hi;
-    q4::range8(w, lo, hi);
+    const uint4* src = reinterpret_cast<const uint4*>((is_v ? p.v_new : p.k_new) + unit * p.T * p.row_bytes);
+    uint4 val[ROWS];
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = t0 + i * kStep;
+        val[i] = t < n && sub < vecs ? __ldcs(src + static_cast<size_t>(t) * vecs + sub) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (!live) return;
-    const q4::RowScale rs = q4::row_scale(lo, hi);
-    bool bad = false;  // (a position whose block-table entry is bad is not written)
-    const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, h, p.lens[b] + t, &bad);
-    if (bad) return;
+    uint32_t range[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const uint32_t w[4] = {val[i].x, val[i].y, val[i].z, val[i].w};
+        range[i] = q4::range8(w);
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) range[i] = q4::max2(range[i], __shfl_xor_sync(0xffffffffu, range[i], o));
+    // The divisions once for all of the group's rows: lane i of every four
+    // works out row i, and hands it to the others.
+    q4::RowScale mine;
+    if constexpr (ROWS == 4) {
+        const int i = sub & 3;
+        mine = q4::row_scale(i < 2 ? (i == 0 ? range[0] : range[1]) : (i == 2 ? range[2] : range[3]));
+    } else {
+        static_assert(ROWS == 1, "one row a lane group, or four");
+        mine = q4::row_scale(range[0]);
+    }
     uint32_t* codes = reinterpret_cast<uint32_t*>(is_v ? p.v_cache : p.k_cache);
-    codes[static_cast<size_t>(row) * vecs + sub] = q4::encode8(w, rs);
-    if (sub == 0) (is_v ? p.q4.v : p.q4.k)[q4::scale_index(p.q4, row)] = rs.word;
+    uint32_t* words = is_v ? p.q4.v : p.q4.k;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = t0 + i * kStep;
+        q4::RowScale rs = mine;
+        if constexpr (ROWS == 4) {
+            rs.inv = __shfl_sync(0xffffffffu, mine.inv, i, 4);
+            rs.word = __shfl_sync(0xffffffffu, mine.word, i, 4);
+            rs.plain = rs.inv != 0.f;  // (a step below 2^126 has a reciprocal above 0)
+        }
+        if (t >= n || sub >= vecs) continue;
+        bool bad = false;  // (a position whose block-table entry is bad is not written)
+        const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, h, p.lens[b] + t, &bad);
+        if (bad) continue;
+        const uint32_t w[4] = {val[i].x, val[i].y, val[i].z, val[i].w};
+        codes[static_cast<size_t>(row) * vecs + sub] = q4::encode8(w, rs);
+        if (sub == 0) words[q4::scale_index(p.q4, row)] = rs.word;
+    }
 }
 
-// KIND as in ReadParams.
-template <int KIND>
+// KIND as in ReadParams; LANES: lanes a row, at least its 16-byte vectors.
+template <int KIND, int LANES, int ROWS>
 __global__ void __launch_bounds__(kThreads) read_rows_kernel(const __grid_constant__ ReadParams p) {
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
+    constexpr int kStep = kThreads / LANES;
     const int b = blockIdx.z, h = blockIdx.y >> 1;
     const bool is_v = (blockIdx.y & 1) != 0;
+    const int n = p.count[b];
     const int vecs = p.d * (KIND == kReadF32 ? 4 : 2) / 16;  // 16-byte vectors of a result row
-    const long long vec = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    if (vec >= static_cast<long long>(p.count[b]) * vecs) return;
-    const int t = static_cast<int>(vec / vecs), c = static_cast<int>(vec - static_cast<long long>(t) * vecs);
-    bool bad = false;  // a bad block-table entry reads as zeros
-    const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, h, p.first[b] + t, &bad);
+    const int c = threadIdx.x % LANES, t0 = blockIdx.x * (kStep * ROWS) + threadIdx.x / LANES;
+    if (t0 >= n || c >= vecs) return;
     const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
-    if (!bad) {
+    const uint32_t* words = is_v ? p.q4.v : p.q4.k;
+    uint4 in[ROWS];       // the vector's stored bytes: 4 (4-bit), 8 (FP8) or 16
+    uint32_t sw[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = t0 + i * kStep;
+        in[i] = make_uint4(0u, 0u, 0u, 0u);
+        sw[i] = 0u;
+        if (t >= n) continue;
+        bool bad = false;  // a bad block-table entry reads as zeros
+        const int row = phys_row(p.pg, p.ring, p.Hkv, p.max_len, b, h, p.first[b] + t, &bad);
+        if (bad) continue;
+        const size_t at = static_cast<size_t>(row) * vecs + c;
         if constexpr (KIND == kReadQ4) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(cache) + static_cast<size_t>(row) * vecs + c);
-            const uint32_t sw = __ldg((is_v ? p.q4.v : p.q4.k) + q4::scale_index(p.q4, row));
-            const float s = q4::step_of(sw);
-            const int z = q4::zero_of(sw);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = ptx::pack_bf16x2(s * static_cast<float>(q4::code_of(w, 2 * i) - z),
-                                        s * static_cast<float>(q4::code_of(w, 2 * i + 1) - z));
+            in[i].x = __ldg(reinterpret_cast<const uint32_t*>(cache) + at);
+            sw[i] = __ldg(words + q4::scale_index(p.q4, row));
         } else if constexpr (KIND == kReadFp8) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) + static_cast<size_t>(row) * vecs + c);
-            const float s = is_v ? p.vscale[h] : p.kscale[h];
-            const uint32_t in[2] = {w.x, w.y};
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) + at);
+            in[i].x = w.x, in[i].y = w.y;
+        } else {
+            in[i] = __ldg(reinterpret_cast<const uint4*>(cache) + at);
+        }
+    }
+    const size_t unit = static_cast<size_t>(b) * p.Hkv + h;
+    uint4* dst = reinterpret_cast<uint4*>(is_v ? p.v_out : p.k_out) + unit * p.T * vecs + c;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
+        const int t = t0 + i * kStep;
+        if (t >= n) continue;
+        uint32_t o[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+        if constexpr (KIND == kReadQ4) {
+            const uint32_t w = in[i].x;
+            const float s = q4::step_of(sw[i]);
+            const int z = q4::zero_of(sw[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = ptx::pack_bf16x2(s * static_cast<float>(q4::code_of(w, 2 * e) - z),
+                                        s * static_cast<float>(q4::code_of(w, 2 * e + 1) - z));
+        } else if constexpr (KIND == kReadFp8) {
+            const float s = is_v ? p.vscale[h] : p.kscale[h];
+            const uint32_t u[2] = {in[i].x, in[i].y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
                 uint32_t f[2];
-                ptx::e4m3x4_to_f16x2x2(in[i], f[0], f[1]);
+                ptx::e4m3x4_to_f16x2x2(u[e], f[0], f[1]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     __half2 hh;
                     memcpy(&hh, &f[j], 4);
                     const float2 v = __half22float2(hh);
-                    o[2 * i + j] = ptx::pack_bf16x2(v.x * s, v.y * s);
+                    o[2 * e + j] = ptx::pack_bf16x2(v.x * s, v.y * s);
                 }
             }
-        } else {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(cache) + static_cast<size_t>(row) * vecs + c);
-            o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
         }
+        __stcs(dst + static_cast<size_t>(t) * vecs, make_uint4(o[0], o[1], o[2], o[3]));
     }
-    const size_t unit = static_cast<size_t>(b) * p.Hkv + h;
-    uint4* dst = reinterpret_cast<uint4*>(is_v ? p.v_out : p.k_out) + unit * p.T * vecs;
-    dst[vec] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename P>
@@ -128,17 +180,40 @@ cudaError_t launch_chained(void (*kernel)(P), dim3 grid, cudaStream_t stream, co
     return cudaGetLastError();
 }
 
+// Grid of a launch over `rows` rows a (K or V, KV head, batch row).
+template <int LANES, int ROWS>
+dim3 rows_grid(int rows, int Hkv, int B) {
+    constexpr int per_block = kThreads / LANES * ROWS;
+    return dim3(static_cast<unsigned>((rows + per_block - 1) / per_block), 2u * Hkv, B);
+}
+
 template <int LANES>
-cudaError_t launch_append_lanes(const AppendParams& p, int max_n_new, cudaStream_t stream) {
-    constexpr int rows = kThreads / LANES;
-    const dim3 grid(static_cast<unsigned>((max_n_new + rows - 1) / rows), 2u * p.Hkv, p.B);
-    return launch_chained(append_q4_kernel<LANES>, grid, stream, p);
+cudaError_t launch_append_lanes(const AppendParams& p, int rows, cudaStream_t stream) {
+    return rows >= kManyRows * (kThreads / LANES)
+               ? launch_chained(append_q4_kernel<LANES, kManyRows>, rows_grid<LANES, kManyRows>(rows, p.Hkv, p.B), stream, p)
+               : launch_chained(append_q4_kernel<LANES, 1>, rows_grid<LANES, 1>(rows, p.Hkv, p.B), stream, p);
+}
+
+template <int KIND, int LANES>
+cudaError_t launch_read_lanes(const ReadParams& p, int rows, cudaStream_t stream) {
+    return rows >= kManyRows * (kThreads / LANES)
+               ? launch_chained(read_rows_kernel<KIND, LANES, kManyRows>, rows_grid<LANES, kManyRows>(rows, p.Hkv, p.B), stream, p)
+               : launch_chained(read_rows_kernel<KIND, LANES, 1>, rows_grid<LANES, 1>(rows, p.Hkv, p.B), stream, p);
+}
+
+template <int KIND>
+cudaError_t launch_read_kind(const ReadParams& p, int rows, cudaStream_t stream) {
+    const int vecs = p.d * (KIND == kReadF32 ? 4 : 2) / 16;  // 1 .. 64
+    if (vecs <= 8) return launch_read_lanes<KIND, 8>(p, rows, stream);
+    if (vecs <= 16) return launch_read_lanes<KIND, 16>(p, rows, stream);
+    if (vecs <= 32) return launch_read_lanes<KIND, 32>(p, rows, stream);
+    return launch_read_lanes<KIND, 64>(p, rows, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_append_q4(const AppendParams& p, int max_n_new, cudaStream_t stream) {
-    const int vecs = p.row_bytes / 16;
+    const int vecs = p.row_bytes / 16;  // 4 .. 32
     if (vecs <= 4) return launch_append_lanes<4>(p, max_n_new, stream);
     if (vecs <= 8) return launch_append_lanes<8>(p, max_n_new, stream);
     if (vecs <= 16) return launch_append_lanes<16>(p, max_n_new, stream);
@@ -146,13 +221,11 @@ cudaError_t launch_append_q4(const AppendParams& p, int max_n_new, cudaStream_t 
 }
 
 cudaError_t launch_read_rows(const ReadParams& p, int max_count, cudaStream_t stream) {
-    const long long vecs = static_cast<long long>(max_count) * (p.d * (p.kind == kReadF32 ? 4 : 2) / 16);
-    const dim3 grid(static_cast<unsigned>((vecs + kThreads - 1) / kThreads), 2u * p.Hkv, p.B);
     switch (p.kind) {
-        case kReadF32: return launch_chained(read_rows_kernel<kReadF32>, grid, stream, p);
-        case kReadBf16: return launch_chained(read_rows_kernel<kReadBf16>, grid, stream, p);
-        case kReadFp8: return launch_chained(read_rows_kernel<kReadFp8>, grid, stream, p);
-        case kReadQ4: return launch_chained(read_rows_kernel<kReadQ4>, grid, stream, p);
+        case kReadF32: return launch_read_kind<kReadF32>(p, max_count, stream);
+        case kReadBf16: return launch_read_kind<kReadBf16>(p, max_count, stream);
+        case kReadFp8: return launch_read_kind<kReadFp8>(p, max_count, stream);
+        case kReadQ4: return launch_read_kind<kReadQ4>(p, max_count, stream);
         default: return cudaErrorInvalidValue;
     }
 }
