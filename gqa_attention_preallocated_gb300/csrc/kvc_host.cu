@@ -82,9 +82,12 @@ namespace {
 // kernel, so there the split-KV kernel (128-key FP8 tiles) leads up to 32
 // rows (2,855 against 2,484 GB/s at 32) and the tcgen05 kernel from 64 (2,524
 // against 1,670).
+// A 4-bit cache: the split-KV kernels unpack a tile once for up to 32 rows and
+// lead there (B = 64, S = 4096: 201 us at 32 rows against 246); two blocks of
+// 32 rows read it twice (361 us at 48 rows against 247).
 constexpr int kTcMinRows = 12;
 constexpr int kTcMinRowsFp8 = 32;
-constexpr int kTcMinRowsQ4 = 16;
+constexpr int kTcMinRowsQ4 = 32;
 int tc_min_rows(const kvc_cache* c) {
     return c->dtype == KVC_Q4 ? kTcMinRowsQ4 : c->dtype == KVC_FP8_E4M3 ? kTcMinRowsFp8 : kTcMinRows;
 }
@@ -277,8 +280,8 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
     pl->generic = generic_call(c, pl->R);
     if (!pl->generic) {
         pl->mt = pl->R <= 16 ? 1 : (pl->R <= 32 ? 2 : 4);
-        // 4-bit caches: blocks of 8 or 16 rows (more rows re-read the tiles).
-        pl->RPB = c->dtype == KVC_Q4 ? (pl->R <= 8 ? 8 : 16) : 16 * pl->mt;
+        // 4-bit caches: blocks of 8, 16, 24 or 32 rows (more rows re-read the tiles).
+        pl->RPB = c->dtype == KVC_Q4 ? std::min(32, std::max(8, (pl->R + 7) / 8 * 8)) : 16 * pl->mt;
         pl->RB = std::max(1, (pl->R + pl->RPB - 1) / pl->RPB);
         // Only the split-KV kernel works in (row, row block) groups.  A call
         // with more than 64 rows per KV head (more than any tree call takes)
@@ -1275,9 +1278,11 @@ static kvc_status append_attention_impl(kvc_cache* c, int layer, const void* q, 
     if (s) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int64_t* lw = c->lens.data() + static_cast<size_t>(layer) * c->B;
-    if (!pl.generic && pl.mt == 1 && max_n > 0 && (pl.R <= tc_min_rows(c) || !tc_capable(c))) {
-        // Warps own whole tiles: the attention kernel writes the new rows into
-        // the cache itself (one launch instead of two).
+    const bool fused = c->dtype == KVC_Q4 ? pl.RB == 1 : pl.mt == 1;
+    if (!pl.generic && fused && max_n > 0 && (pl.R <= tc_min_rows(c) || !tc_capable(c))) {
+        // Warps own whole tiles (4-bit caches: one row block holds every query
+        // row), so each tile is processed once: the attention kernel writes the
+        // new rows into the cache itself (one launch instead of two).
         for (int b = 0; b < c->B; ++b) lw[b] += n_new[b];
         bool enqueued = false;
         s = do_attention(c, layer, q, pl, n_new, out, workspace, workspace_bytes, st, k_new, v_new, &enqueued, ancp);

@@ -221,8 +221,10 @@ DecodeLaunch decode_launch_shape(int mt, bool fp8, int d);
 
 cudaError_t launch_decode_bf16(const DecodeParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV, int mt,
                                int grid, bool fp8, int d, cudaStream_t stream);
-// 4-bit caches: row blocks of p.RPB = 8 or 16, one partial sub-slot per (unit, CTA).
+// 4-bit caches: row blocks of p.RPB = 8, 16, 24 or 32, one partial sub-slot per
+// (unit, CTA).
 cudaError_t launch_decode_q4(const DecodeParams& p, int grid, int d, cudaStream_t stream);
+cudaError_t launch_decode_q4_wide(const DecodeParams& p, int grid, cudaStream_t stream);  // d = 128, RPB > 8
 
 // ---------------------------------------------------------------------------
 // f32 attention (any d <= 256, d % 4 == 0): one CTA per (16-row block, kvh, b),
