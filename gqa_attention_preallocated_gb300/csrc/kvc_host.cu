@@ -280,8 +280,13 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
     pl->generic = generic_call(c, pl->R);
     if (!pl->generic) {
         pl->mt = pl->R <= 16 ? 1 : (pl->R <= 32 ? 2 : 4);
-        // 4-bit caches: blocks of 8, 16, 24 or 32 rows (more rows re-read the tiles).
-        pl->RPB = c->dtype == KVC_Q4 ? std::min(32, std::max(8, (pl->R + 7) / 8 * 8)) : 16 * pl->mt;
+        pl->RPB = 16 * pl->mt;
+        if (c->dtype == KVC_Q4) {
+            // One block of 8, 16, 24 or 32 rows (mt 1), or several of 32, which
+            // each read the tiles.
+            pl->mt = pl->R <= 32 ? 1 : 2;
+            pl->RPB = std::min(32, std::max(8, (pl->R + 7) / 8 * 8));
+        }
         pl->RB = std::max(1, (pl->R + pl->RPB - 1) / pl->RPB);
         // Only the split-KV kernel works in (row, row block) groups.  A call
         // with more than 64 rows per KV head (more than any tree call takes)
@@ -1278,8 +1283,7 @@ static kvc_status append_attention_impl(kvc_cache* c, int layer, const void* q, 
     if (s) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int64_t* lw = c->lens.data() + static_cast<size_t>(layer) * c->B;
-    const bool fused = c->dtype == KVC_Q4 ? pl.RB == 1 : pl.mt == 1;
-    if (!pl.generic && fused && max_n > 0 && (pl.R <= tc_min_rows(c) || !tc_capable(c))) {
+    if (!pl.generic && pl.mt == 1 && max_n > 0 && (pl.R <= tc_min_rows(c) || !tc_capable(c))) {
         // Warps own whole tiles (4-bit caches: one row block holds every query
         // row), so each tile is processed once: the attention kernel writes the
         // new rows into the cache itself (one launch instead of two).
@@ -1580,8 +1584,8 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     s = plan_shape(c, q_heads, T, c->num_sms, &pl);
     if (s) return s;
     if (pl.mt != 1)
-        return fail(KVC_ERR_SHAPE, "device-resident steps take G * T <= 16 query rows per KV head (G * T = %d)",
-                    pl.R);
+        return fail(KVC_ERR_SHAPE, "device-resident steps take G * T <= %d query rows per KV head (G * T = %d)",
+                    c->dtype == KVC_Q4 ? 32 : 16, pl.R);
     if (static_cast<long long>(pl.NB) * ((c->max_len + kKeyTile - 1) / kKeyTile) * c->Hkv > 0x7fffffffll)
         return fail(KVC_ERR_ARG, "too many key tiles for one call");
     s = check_workspace(c, pl, workspace, workspace_bytes);

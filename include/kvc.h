@@ -449,14 +449,15 @@ kvc_status kvc_lens_from_device(kvc_cache* c, void* stream);
  * the T queries q [B, Hq, T, d] attend exactly as in kvc_gqa_attention, and
  * the device lengths advance by n_new.  n_new is a device int32 [B].  bf16
  * and FP8 caches of d = 128, and bf16 caches of d = 64, with G * T <= 16 query
- * rows per KV head (decode and short verify).
+ * rows per KV head (decode and short verify); 4-bit caches of d = 64 and 128
+ * with G * T <= 32.
  * Three kernels are enqueued (device plan, attention with the append fused
  * in, combine), with nothing read from the host that changes per step, so
  * the call can be captured in a CUDA graph and replayed with new contents of
  * q, k_new, v_new and n_new.  The workspace is the one kvc_workspace_bytes
  * sizes (plus its device plan region, included there).
  * Errors found on the host (nothing enqueued): KVC_ERR_ARG (lengths on the
- * host, pointers, dtype), KVC_ERR_SHAPE (G * T > 16, Hq % Hkv), KVC_ERR_WORKSPACE,
+ * host, pointers, dtype), KVC_ERR_SHAPE (G * T > 16, or 32; Hq % Hkv), KVC_ERR_WORKSPACE,
  * KVC_ERR_CUDA.  A row with n_new[b] outside 0..T or past max_len rejects the
  * whole step on the device: nothing is written, no length changes, and the
  * next kvc_device_status returns KVC_ERR_OVERFLOW. */

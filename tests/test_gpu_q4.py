@@ -33,12 +33,17 @@ def _bf(x):
 
 
 def _attend(q, K, V, lens, n_new, window=0, parents=None):
-    """(out, sum p |v| / sum p, largest sum |q k| / sqrt d over a query's keys) in float64.
+    """(out, sum p |v| / sum p, largest sum |q k| / sqrt d over a query's keys, f32 sums' error) in float64.
 
-    q [B, Hq, T, d]; K, V: per row [Hkv, len, d], row b's tokens at their positions."""
+    q [B, Hq, T, d]; K: per row values [Hkv, len, d], V: per row (values, steps [Hkv, len]), row b's tokens at
+    their positions.
+
+    The last is what adding in float32 may lose: out is sum p s c - sum p s z, both sums of terms up to
+    15 p s, added 16 keys at a time by the tensor core (which may truncate: 2^-23 of the sum an addition)
+    and a few keys a thread.  So each loses at most (L / 16 + 16) 2^-23 of 15 sum p s."""
     B, Hq, T, d = q.shape
     out, mass = np.zeros(q.shape), np.zeros(q.shape)
-    dot = np.zeros((B, Hq, T, 1))
+    dot, add = np.zeros((B, Hq, T, 1)), np.zeros((B, Hq, T, 1))
     for b in range(B):
         n, L = int(n_new[b]), int(lens[b])
         if n == 0:
@@ -60,27 +65,29 @@ def _attend(q, K, V, lens, n_new, window=0, parents=None):
             x = np.where(see[None], x, -np.inf)
             p = np.exp(x - x.max(-1, keepdims=True))
             p /= p.sum(-1, keepdims=True)
-            Vh = np.where(see.any(0)[:, None], V[b][h], 0.0)
+            Vh = np.where(see.any(0)[:, None], V[b][0][h], 0.0)
+            Sh = np.where(see.any(0), V[b][1][h], 0.0)
+            add[b, h * G:(h + 1) * G, :n, 0] = (p @ Sh) * 15 * (L / 16 + 16) * 2.0 ** -22
             out[b, h * G:(h + 1) * G, :n] = p @ Vh
             mass[b, h * G:(h + 1) * G, :n] = p @ np.abs(Vh)
             a = np.einsum("gtd,sd->gts", np.abs(q[b, h * G:(h + 1) * G, :n]), np.abs(K[b][h])) / math.sqrt(d)
             dot[b, h * G:(h + 1) * G, :n, 0] = np.where(see[None], a, 0.0).max(-1)
-    return out, mass, dot
+    return out, mass, dot, add
 
 
-def _bound(want, mass, dot, rows):
+def _bound(want, mass, dot, add, rows):
     """Largest |got - want| that the kernels' roundings allow.
 
-    The output is rounded to bf16.  Up to 16 query rows per KV head the codes
-    and queries enter the products exactly and only the softmax weights are
+    The output is rounded to bf16.  Up to 32 query rows per KV head (and in
+    trees) the codes and queries enter the products exactly and only the softmax weights are
     rounded, to f16.  Above, the rows are rounded to bf16 on their way to the
     tensor core (K: each score moves by at most UB * sum |q k| / sqrt d, so each
     weight by twice that; V: by UB) and the weights too.  float32 sums, exp2
     and the norm add 2^-16 of the mass, and 2^-20 * sum |q k| / sqrt d in the
     scores."""
-    up, uv, uk = (U16, 0.0, 0.0) if rows <= 16 else (UB, UB, UB)
+    up, uv, uk = (U16, 0.0, 0.0) if rows <= 32 else (UB, UB, UB)
     shift = 2 * np.expm1((uk + 2.0 ** -20) * dot)
-    return UB * np.abs(want) + mass * (1 + UB) * (up + uv + shift + 2.0 ** -16) + 1e-30
+    return UB * np.abs(want) + mass * (1 + UB) * (up + uv + shift + 2.0 ** -16) + add + 1e-30
 
 
 class Pair:
@@ -123,16 +130,18 @@ class Pair:
                 x[b] = np.concatenate([x[b], new[b, :, : int(n_new[b])]], axis=1)
 
     def values(self):
-        return [[ref.q4_store(r) for r in x] for x in self.x]
+        """K values, and V (values, steps), per row."""
+        V = [ref.q4_quantize(r) for r in self.x[1]]
+        return [ref.q4_store(r) for r in self.x[0]], [(ref.q4_values(*v), v[1]) for v in V]
 
     def check_out(self, out, q, n_new, T, parents=None, tag=""):
         K, V = self.values()
-        want, mass, dot = _attend(q.double().numpy(), K, V, self.lens, n_new, self.window, parents)
+        want, *about = _attend(q.double().numpy(), K, V, self.lens, n_new, self.window, parents)
         got = out.double().cpu().numpy()
         for b in range(self.B):
             assert np.all(got[b, :, int(n_new[b]):] == 0.0), (tag, b)
         G = q.shape[1] // self.Hkv
-        lim = _bound(want, mass, dot, G * T)
+        lim = _bound(want, *about, G * T)
         over = np.abs(got - want) - lim
         assert np.isfinite(got).all(), tag
         assert over.max() <= 0, (tag, float(over.max()), float(np.abs(got - want).max()))
@@ -399,12 +408,12 @@ def test_layers_truncate_and_host_buffers():
     p.check_out(out, q, [2, 1], 3)
 
 
-@pytest.mark.parametrize("d,G,page", [(128, 4, 0), (64, 4, 0), (128, 8, 128), (128, 3, 0)])
-def test_device_steps_and_graph(d, G, page):
+@pytest.mark.parametrize("d,G,page,T", [(128, 4, 0, 2), (64, 4, 0, 2), (128, 8, 128, 1), (128, 3, 0, 2), (128, 4, 0, 6),
+                                        (64, 8, 128, 4), (128, 16, 0, 2)])
+def test_device_steps_and_graph(d, G, page, T):
     """Device-resident lengths: steps run eagerly and replayed from a graph, a rejected step, and the lengths back."""
     p = Pair(3, 2, d, 256, page=page, seed=d + G)
     p.step([100, 0, 126], G)
-    T = 2 if G * 2 <= 16 else 1
     q, k, v = (torch.zeros(3, H, T, d, dtype=torch.bfloat16, device="cuda") for H in (2 * G, 2, 2))
     n = torch.zeros(3, dtype=torch.int32, device="cuda")
     out, ws = torch.zeros_like(q), torch.zeros(p.c.workspace_bytes(2 * G, T), dtype=torch.uint8, device="cuda")
@@ -420,9 +429,9 @@ def test_device_steps_and_graph(d, G, page):
     def check(i, n_new):
         p.note(i[1], i[2], n_new)
         K, V = p.values()
-        want, mass, dot = _attend(i[0].double().numpy(), K, V, p.lens, n_new)
+        want, *about = _attend(i[0].double().numpy(), K, V, p.lens, n_new)
         got = out.double().cpu().numpy()
-        assert (np.abs(got - want) - _bound(want, mass, dot, G * T)).max() <= 0
+        assert (np.abs(got - want) - _bound(want, *about, G * T)).max() <= 0
         assert p.c.device_status(ws) == 0
 
     i = feed([T, 1, 0])
