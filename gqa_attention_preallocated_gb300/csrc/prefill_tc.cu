@@ -26,12 +26,11 @@
 // into the softmax scale and the V scale into the output normalisation.
 //
 // 4-bit caches (KVC_Q4; also d = 64): a tile's codes and scale words arrive by
-// untiled copies in raw slots, two for K and one for V (its converters hold
-// the next tile in registers while they wait for its stage); two warps convert
-// K and two more V into the bf16 tiles the MMAs read.  K and V have slots of
-// their own because an mbarrier's parity cannot tell phases two apart: a slot
-// that both used would let the converters that run ahead read it early.  A value is
-// s * (c - z), rounded once to bf16: c - z is exact in bf16 and one product
+// untiled copies in raw slots, two for K and one for V, and four warps, a row a
+// thread, convert K, then V, into the bf16 tiles the MMAs read (all four on one
+// tensor: two warps for each of K and V took 236 us where this takes 207, B = 64,
+// S = 4096, 64 rows, as a tile's conversion stands in the way of its products).
+// A value is s * (c - z), rounded once to bf16: c - z is exact in bf16 and one product
 // rounds it, so the MMAs see what kvc_read gives.  (Folding the step into the
 // softmax instead, as the split-KV kernel does, would cost a multiply a score
 // and a weight, 256 rows x 128 keys a tile, where the conversion's is one a
@@ -48,7 +47,7 @@
 //               P_i as the TMEM A operand.  Issue order S0(j), S1(j), PV0(j),
 //               S0(j+1), PV1(j), S1(j+1), ... keeps the tensor core busy while
 //               each softmax warpgroup works on the other head's tile.
-//   warps 2, 3  FP8: converters; 4-bit: converters of K (12, 13: of V)
+//   warps 2, 3  FP8: converters; 4-bit: converters, with warps 12, 13
 //   warps 4-7   softmax of row tile 0 (mode 2: even key tiles), one thread per query row
 //   warps 8-11  softmax of row tile 1 (mode 2: odd key tiles)
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).
@@ -131,62 +130,53 @@ __device__ __forceinline__ uint32_t instr_desc(bool b_mn_major, bool f16, int n)
     return (1u << 4) | ab | (static_cast<uint32_t>(b_mn_major) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// 4-bit caches: rows r and r + 64 of a raw slot (d / 2 bytes a row) into the
-// bf16 tile the MMAs read (64-column boxes, 128-byte swizzle).  A thread owns
-// whole rows and takes its 16-byte pieces in an order that starts at r / 2, so
-// that eight neighbouring rows read eight different bank groups (their strides
-// are 64 bytes) and write eight too.
+// 4-bit caches: row r of a raw slot (d / 2 bytes a row) into the bf16 tile the
+// MMAs read (64-column boxes, 128-byte swizzle).  A thread owns a row and takes
+// its 16-byte pieces in an order that starts at r / 2, so that eight
+// neighbouring rows read eight different bank groups (their strides are 64
+// bytes) and write eight too.
 template <int kDim>
-struct RawRows {
+struct RawRow {
     static constexpr int kPieces = kDim / 32;  // 16-byte pieces of a row: 32 codes
-    uint4 w[2][kPieces];
-    uint32_t own[2], other[2];  // the row's scale word, and the other tensor's
-    __device__ __forceinline__ void load(const uint8_t* raw, int ct, bool is_v) {
+    uint4 w[kPieces];
+    uint32_t own, other;  // the row's scale word, and the other tensor's
+    __device__ __forceinline__ void load(const uint8_t* raw, int r, bool is_v) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = ct + 64 * h;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                w[h][i] = *reinterpret_cast<const uint4*>(raw + r * (kDim / 2) + ((i + (r >> 1)) % kPieces) * 16);
-            const uint32_t k = *reinterpret_cast<const uint32_t*>(raw + kRawScaleK + r * 4);
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(raw + kRawScaleV + r * 4);
-            own[h] = is_v ? v : k;
-            other[h] = is_v ? k : v;
-        }
+        for (int i = 0; i < kPieces; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(raw + r * (kDim / 2) + ((i + (r >> 1)) % kPieces) * 16);
+        const uint32_t k = *reinterpret_cast<const uint32_t*>(raw + kRawScaleK + r * 4);
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(raw + kRawScaleV + r * 4);
+        own = is_v ? v : k;
+        other = is_v ? k : v;
     }
-    __device__ __forceinline__ void convert(uint8_t* tile, int ct, bool is_v) const {
+    __device__ __forceinline__ void convert(uint8_t* tile, int r, bool is_v) const {
+        auto is_nan = [](uint32_t word) { return (word & 0x7FFF0000u) >= 0x7F800000u; };
+        uint32_t s = __byte_perm(own, 0, 0x3232);  // the step in both halves
+        if (is_v) {
+            if (is_nan(own)) s = 0u;
+        } else if (is_nan(other)) {
+            s = 0x7FC07FC0u;
+        }
+        const uint32_t z = 0x43004300u + (own & 0xFFu) * 0x00010001u;  // 128 + z, twice
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = ct + 64 * h;
-            auto is_nan = [](uint32_t word) { return (word & 0x7FFF0000u) >= 0x7F800000u; };
-            uint32_t s = __byte_perm(own[h], 0, 0x3232);  // the step in both halves
-            if (is_v) {
-                if (is_nan(own[h])) s = 0u;
-            } else if (is_nan(other[h])) {
-                s = 0x7FC07FC0u;
-            }
-            const uint32_t z = 0x43004300u + (own[h] & 0xFFu) * 0x00010001u;  // 128 + z, twice
+        for (int i = 0; i < kPieces; ++i) {
+            const int piece = (i + (r >> 1)) % kPieces;
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int piece = (i + (r >> 1)) % kPieces;
-                const uint32_t u[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+            for (int k = 0; k < 4; ++k) {  // word k: columns 32 piece + 8k .. + 7
+                uint32_t o[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // word k: columns 32 piece + 8k .. + 7
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t c = ((u[k] >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + c, twice
-                        o[e] = ptx::mul_bf16x2(ptx::sub_bf16x2(c, z), s);
-                    }
-                    const int cc = piece * 4 + k;  // 16-byte chunk of the row
-                    *reinterpret_cast<uint4*>(tile + (cc >> 3) * kBoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t c = ((u[k] >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + c, twice
+                    o[e] = ptx::mul_bf16x2(ptx::sub_bf16x2(c, z), s);
                 }
+                const int cc = piece * 4 + k;  // 16-byte chunk of the row
+                *reinterpret_cast<uint4*>(tile + (cc >> 3) * kBoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
     }
 };
-
 
 // FP8 caches: one 128-key tile of E4M3 codes (128 rows x 128 bytes, 128-byte
 // swizzle) sits in the second half of a stage; convert it in place to the f16
@@ -554,11 +544,11 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        const int ready = kF8 || kQ4 ? 2 : 1;  // both converter warps arrive; else the TMA's arrive
+        const int ready = kQ4 ? 4 : kF8 ? 2 : 1;  // every converter warp arrives; else the TMA's arrive
         ptx::mbar_init(bar(kBarQ), kF8 ? 2 : 1);
         for (int s = 0; s < kRawSlots && kQ4; ++s) {
             ptx::mbar_init(bar(kBarRawFull + s), 1);
-            ptx::mbar_init(bar(kBarRawEmpty + s), 2);
+            ptx::mbar_init(bar(kBarRawEmpty + s), 4);
         }
         ptx::mbar_init(bar(kBarQRaw), 1);
         for (int s = 0; s < 2; ++s) {
@@ -732,28 +722,30 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
         }
     } else if (kQ4 && (warp == 2 || warp == 3 || warp >= 12)) {
         // ------------------------------------------------------------ 4-bit -> bf16 converters
-        const bool is_v = warp >= 12;
-        const int ct = (is_v ? tid - 384 : tid - 64);
+        const int r = warp >= 12 ? tid - 320 : tid - 64;  // this thread's row of a tile
         auto wait_for = [&](int b_idx, int parity) {
             if (!ptx::mbar_wait_bounded(bar(b_idx), parity, *abort_flag ? 0ull : kWaitNs)) {
                 atomicExch(p.err, kDevTimeoutFull);
                 *abort_flag = 1;
             }
         };
-        const int tile0 = is_v ? kOffV : kOffK, bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
-        for (int j = 0; j < nkt; ++j) {
+        auto convert = [&](int j, bool is_v) {
+            // (K and V have slots of their own, and each slot's uses come to these
+            // warps in order: an mbarrier's parity cannot tell phases two apart.)
             const int s = j & 1, sl = is_v ? 2 : s, turn = is_v ? j : j >> 1;
-            RawRows<kD> rows;
+            RawRow<kD> row;
             wait_for(kBarRawFull + sl, turn & 1);
-            rows.load(smem + kOffRaw + sl * kRawBytes, ct, is_v);
+            row.load(smem + kOffRaw + sl * kRawBytes, r, is_v);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));
-            if (j >= 2) wait_for(bar_empty + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
-            rows.convert(smem + tile0 + s * kTile128, ct, is_v);
+            if (j >= 2) wait_for((is_v ? kBarVEmpty : kBarKEmpty) + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
+            row.convert(smem + (is_v ? kOffV : kOffK) + s * kTile128, r, is_v);
             ptx::fence_proxy_async_smem();  // generic writes -> visible to the tensor core
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar(bar_full + s));
-        }
+            if (lane == 0) ptx::mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + s));
+        };
+#pragma unroll 1
+        for (int n = 0; n < 2 * nkt; ++n) convert(n >> 1, (n & 1) != 0);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t id_qk = instr_desc(false, kF8, 128), id_pv = instr_desc(true, kF8, kD);
