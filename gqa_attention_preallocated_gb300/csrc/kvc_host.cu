@@ -107,6 +107,8 @@ int split_tile_keys(const kvc_cache* c) {
 // Calls with more query rows per KV head than the split-KV kernel's 64 on a
 // cache the tensor-core kernel cannot take (bf16, d = 64) run on the generic kernel.
 bool generic_call(const kvc_cache* c, int R) { return generic_path(c) || (!tc_capable(c) && R > 64); }
+// 4-bit caches: blocks of this many pieces are merged by a launch of their own.
+constexpr int kDeferPieces = 4;
 constexpr int kTcMaxLen = 0xFFFF * 128;  // key tiles of a piece are packed in 16 bits
 
 thread_local std::string g_last_error;
@@ -500,8 +502,9 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         // from HBM about once and then hit in L2.
         static_assert(sizeof(PrefillParams) < 32000, "kernel parameter block too large");
         struct WorkItem {
-            int code, kt0, nkt, nh;  // key tiles kt0 .. nkt - 1 (absolute position / 128)
+            int code, kt0, nkt, nh;  // key tiles kt0 .. nkt - 1 (absolute position / 128), cost of one
         };
+        auto tile_cost = [&](int row_tiles) { return c->dtype == KVC_Q4 ? 2 + row_tiles : row_tiles; };
         std::vector<WorkItem> items;
         PrefillParams pp;
         pp.q = q;
@@ -522,6 +525,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 pp.vscale[h] = c->vscale[static_cast<size_t>(layer) * c->Hkv + h];
             }
         pp.d = c->d;
+        pp.defer_pieces = c->dtype == KVC_Q4 ? kDeferPieces : 0;
         pp.q4 = q4_scales(c, layer);
         pp.k_cache = static_cast<const uint8_t*>(c->k[layer]);
         pp.v_cache = static_cast<const uint8_t*>(c->v[layer]);
@@ -542,7 +546,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 for (int pr = 0; pr < pp.npair; ++pr) {
                     const int code = (b * c->Hkv + kvh) * pp.npair + pr;
                     const int cost = pp.mode == 2 ? 1 : std::min(2, (pl.R - pr * 256 + 127) / 128);
-                    items.push_back({code, kfirst / 128, kmax / 128 + 1, cost});
+                    items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(cost)});
                 }
             }
             for (int kvh = 0; kvh < c->Hkv && pp.mode == 0; ++kvh)
@@ -554,7 +558,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                     const int kfirst = c->window > 0 ? std::max(0, pp.prior[b] + t0 - c->window + 1) : 0;
                     for (int pr = 0; pr < pp.npair; ++pr) {
                         const int code = ((b * c->Hkv + kvh) * pp.ntb + tb) * pp.npair + pr;
-                        items.push_back({code, kfirst / 128, kmax / 128 + 1, std::min(2, pl.G - 2 * pr)});
+                        items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(std::min(2, pl.G - 2 * pr))});
                     }
                 }
         }
@@ -581,12 +585,22 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 // time as 5.1 us + 1.02 us per tile x head, so start-up is 5 units (13 and 8
                 // were 1 to 10 % slower); pieces of 16 tiles were 1 to 4 % slower, pieces of
                 // 4 tiles the same.
-                constexpr long long kStartCost = 5;
-                constexpr int kMinPieceTiles = 8;
+                // A 4-bit cache's items cost more to start (the first tiles wait for
+                // their conversion) and more a tile with one row tile (the
+                // conversion serves one and not two): 3 and 4 units a tile, start-up
+                // 14.  With fewer items than SMs its pieces may be of 4 tiles, as
+                // blocks of many pieces are merged by a launch of their own (333
+                // queries of 3 heads behind 4000 tokens: 78 us with the units above
+                // and pieces of 8, 61 with these; with more items than SMs pieces of
+                // 4 were 3 % slower).
+                const bool q4 = c->dtype == KVC_Q4;
+                const long long kStartCost = q4 ? 14 : 5;
+                const int kMinPieceTiles = q4 && n_items < nsm ? 4 : 8;
                 long long W = 0;
                 for (size_t k = i0; k < i1; ++k)
                     W += static_cast<long long>(items[k].nkt - items[k].kt0) * items[k].nh + kStartCost;
-                const long long target = W / nsm + kStartCost;  // the SMs' common finishing time
+                // The SMs' common finishing time (at least a shortest piece's).
+                const long long target = std::max<long long>(W / nsm, q4 ? 4 * kMinPieceTiles : 0) + kStartCost;
                 // Remaining parts of items, longest first (ties: item order).
                 struct Part {
                     long long cost;
@@ -658,6 +672,11 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 ++c->launches;
                 launched = true;
                 if (main_enqueued) *main_enqueued = true;
+                if (pp.defer_pieces > 0 && *std::max_element(npieces.begin(), npieces.end()) >= pp.defer_pieces) {
+                    e = launch_prefill_combine(pp, stream);
+                    if (e != cudaSuccess) return cuda_fail(e, "prefill combine launch");
+                    ++c->launches;
+                }
             }
         }
         if (launched) return ok();

@@ -298,6 +298,9 @@ struct PrefillParams {
     Paging pg;
     float scale_log2;
     int d;             // 128, or 64 for a 4-bit cache
+    // Blocks cut into this many pieces or more are left as partials, which
+    // launch_prefill_combine merges (0: the last piece to finish always merges).
+    int defer_pieces;
     Q4Scales q4;       // 4-bit cache: the rows' scale words (k null otherwise) and their codes
     const uint8_t *k_cache, *v_cache;
     int prior[kMaxBatch];
@@ -312,6 +315,9 @@ struct PrefillParams {
 
 cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                               const CUtensorMap& tmV, cudaStream_t stream);
+
+// Merge of the blocks that the prefill launch left as partials (p.defer_pieces).
+cudaError_t launch_prefill_combine(const PrefillParams& p, cudaStream_t stream);
 
 // Device error codes written to the workspace error word.
 enum DeviceError : int {

@@ -369,7 +369,7 @@ __device__ __forceinline__ Piece decode_piece(const PrefillParams& p, int idx) {
 template <int kD>
 __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t tS, uint32_t tO, int i, int r, bool valid,
                                             float m_ref, float l, int slot, int kidx, int npc, __nv_bfloat16* dst,
-                                            volatile int* merge_flag, float out_scale, float* stage) {
+                                            volatile int* merge_flag, float out_scale, float* stage, bool defer) {
     constexpr int kRowF = kD + 4;             // floats per partial row: O, m, l, pad
     constexpr int kChunks = 128 * kRowF / 4;  // 16-byte chunks of one head's block
     static_assert(kChunks % 128 == 0, "each thread moves the same number of chunks");
@@ -397,6 +397,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
 #pragma unroll 3
         for (int x = r; x < kChunks; x += 128) g[x] = s4[x];
     }
+    if (defer) return;  // merged by a launch of its own
     __threadfence();
     ptx::named_barrier_sync(1 + i, 128);
     int* counter = err + kWsCounterOffset / sizeof(int) + slot0 * 2 + i;
@@ -1021,7 +1022,8 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             } else if (pc.slot != kPrefillNoSlot) {
                 split_epilogue<kD>(p.partials, p.err, tS, tO, i, r, valid, m_ref, l, pc.slot, pc.kidx, pc.npc, dst, merge_flag,
                                kF8 ? p.vscale[kvh] : 1.f,
-                               reinterpret_cast<float*>(smem + kOffQ + i * kSplitStageBytes));
+                               reinterpret_cast<float*>(smem + kOffQ + i * kSplitStageBytes),
+                               p.defer_pieces > 0 && pc.npc >= p.defer_pieces);
             } else {
             const float inv = (valid && l > 0.f) ? (kF8 ? p.vscale[kvh] : 1.f) / l : 0.f;
 #pragma unroll
@@ -1056,6 +1058,51 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
 }  // namespace
 
 namespace {
+
+// Merge of a block cut into many pieces: o = sum_k 2^(m_k - M) O_k / sum_k
+// 2^(m_k - M) l_k, the pieces in their order.  The last piece of such a block
+// would read all the others by itself while the other SMs stand idle (2 us a
+// piece: 38 pieces of one KV head's 400 rows, 98 us in all against 38 with this
+// launch); here a warp takes a row.
+constexpr int kCombineWarps = 8;
+template <int kD>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_pieces_kernel(const __grid_constant__ PrefillParams p) {
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const Piece pc = decode_piece(p, blockIdx.x);
+    if (pc.slot == kPrefillNoSlot || pc.kidx != 0 || pc.npc < p.defer_pieces) return;
+    constexpr int kRowF = kD + 4, kPer = kD / 32;  // floats of a partial row, output dims a lane
+    const int lane = threadIdx.x & 31, r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+    for (int i = 0; i < pc.nh; ++i) {
+        const int pr = pc.pr0 + i * 128 + r;  // modes 1, 2: packed row g*T + t of the KV head
+        const int t = p.mode == 0 ? pc.t0 + r : pr % p.T;
+        if (t >= pc.nn || t >= p.T || (p.mode != 0 && pr >= p.G * p.T)) continue;
+        const float* part = p.partials + (static_cast<size_t>(pc.slot) * 2 + i) * 128 * kRowF + static_cast<size_t>(r) * kRowF;
+        constexpr size_t kStep = static_cast<size_t>(2) * 128 * kRowF;  // the next piece's row
+        float M = -INFINITY;
+        for (int k = lane; k < pc.npc; k += 32) M = fmaxf(M, __ldcg(part + k * kStep + kD));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float L = 0.f, acc[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < pc.npc; ++k) {
+            const float* pk = part + k * kStep;
+            const float w = ptx::ex2(__ldcg(pk + kD) - Mu);
+            L = fmaf(w, __ldcg(pk + kD + 1), L);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, __ldcg(pk + lane * kPer + e), acc[e]);
+        }
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // (NaN stays)
+        const size_t row = p.mode == 0 ? static_cast<size_t>(pc.b * p.Hq + pc.h0 + i) * p.T + t
+                                       : static_cast<size_t>(pc.b * p.Hq + pc.h0) * p.T + pr;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * kD + lane * kPer);
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) dst[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
 
 template <int kFmt, int kD>
 cudaError_t launch_fmt(const PrefillParams& p, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
@@ -1097,6 +1144,21 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, co
         return p.d == 64 ? launch_fmt<kFmtQ4, 64>(p, tmQ, tmQ, tmQ, stream) : launch_fmt<kFmtQ4, 128>(p, tmQ, tmQ, tmQ, stream);
     }
     return p.fp8 ? launch_fmt<kFmtFp8, 128>(p, tmQ, tmK, tmV, stream) : launch_fmt<kFmtBf16, 128>(p, tmQ, tmK, tmV, stream);
+}
+
+cudaError_t launch_prefill_combine(const PrefillParams& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_pieces, 128 / kCombineWarps);
+    cfg.blockDim = dim3(kCombineWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, p.d == 64 ? combine_pieces_kernel<64> : combine_pieces_kernel<128>, p);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
 }
 
 }  // namespace kvc
