@@ -71,6 +71,7 @@
 
 #include <math.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "kvc_internal.h"
@@ -1072,36 +1073,58 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_pieces_kernel(cons
     const Piece pc = decode_piece(p, blockIdx.x);
     if (pc.slot == kPrefillNoSlot || pc.kidx != 0 || pc.npc < p.defer_pieces) return;
     constexpr int kRowF = kD + 4, kPer = kD / 32;  // floats of a partial row, output dims a lane
-    const int lane = threadIdx.x & 31, r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-    for (int i = 0; i < pc.nh; ++i) {
-        const int pr = pc.pr0 + i * 128 + r;  // modes 1, 2: packed row g*T + t of the KV head
-        const int t = p.mode == 0 ? pc.t0 + r : pr % p.T;
-        if (t >= pc.nn || t >= p.T || (p.mode != 0 && pr >= p.G * p.T)) continue;
-        const float* part = p.partials + (static_cast<size_t>(pc.slot) * 2 + i) * 128 * kRowF + static_cast<size_t>(r) * kRowF;
-        constexpr size_t kStep = static_cast<size_t>(2) * 128 * kRowF;  // the next piece's row
-        float M = -INFINITY;
-        for (int k = lane; k < pc.npc; k += 32) M = fmaxf(M, __ldcg(part + k * kStep + kD));
+    using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5), i = blockIdx.z;
+    const int pr = pc.pr0 + i * 128 + r;  // modes 1, 2: packed row g*T + t of the KV head
+    const int t = p.mode == 0 ? pc.t0 + r : pr % p.T;
+    if (i >= pc.nh || t >= pc.nn || t >= p.T || (p.mode != 0 && pr >= p.G * p.T)) return;
+    const float* part = p.partials + (static_cast<size_t>(pc.slot) * 2 + i) * 128 * kRowF + static_cast<size_t>(r) * kRowF;
+    constexpr size_t kStep = static_cast<size_t>(2) * 128 * kRowF;  // the next piece's row
+    // 32 pieces at a time: a lane's piece's (m, l), then every piece's O, eight
+    // loads in flight, with the weights handed round; the state (M, L, acc)
+    // carries over.
+    float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < pc.npc; k0 += 32) {
+        const int n = min(32, pc.npc - k0);
+        const float2 ml = lane < n ? __ldcg(reinterpret_cast<const float2*>(part + (k0 + lane) * kStep + kD)) : make_float2(-INFINITY, 0.f);
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float old = M;
+        M = fmaxf(M, top);
         const float Mu = M == -INFINITY ? 0.f : M;
-        float L = 0.f, acc[kPer];
+        const float f = ptx::ex2(old - Mu);  // (0 before the first)
+        const float w = lane < n ? ptx::ex2(ml.x - Mu) : 0.f;
+        float ls = w * ml.y;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < pc.npc; ++k) {
-            const float* pk = part + k * kStep;
-            const float w = ptx::ex2(__ldcg(pk + kD) - Mu);
-            L = fmaf(w, __ldcg(pk + kD + 1), L);
+        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        L = fmaf(L, f, ls);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, __ldcg(pk + lane * kPer + e), acc[e]);
+        for (int e = 0; e < kPer; ++e) acc[e] *= f;
+        for (int k = 0; k < n; k += 8) {
+            Vec v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k + u < n) v[u] = __ldcg(reinterpret_cast<const Vec*>(part + (k0 + k + u) * kStep) + lane);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float wk = __shfl_sync(0xffffffffu, w, k + u);
+                if (k + u < n) {
+                    const float* x = reinterpret_cast<const float*>(&v[u]);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wk, x[e], acc[e]);
+                }
+            }
         }
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // (NaN stays)
-        const size_t row = p.mode == 0 ? static_cast<size_t>(pc.b * p.Hq + pc.h0 + i) * p.T + t
-                                       : static_cast<size_t>(pc.b * p.Hq + pc.h0) * p.T + pr;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * kD + lane * kPer);
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) dst[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
     }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // (NaN stays)
+    const size_t row = p.mode == 0 ? static_cast<size_t>(pc.b * p.Hq + pc.h0 + i) * p.T + t
+                                   : static_cast<size_t>(pc.b * p.Hq + pc.h0) * p.T + pr;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * kD + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) dst[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
 template <int kFmt, int kD>
@@ -1148,7 +1171,7 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, const CUtensorMap& tmQ, co
 
 cudaError_t launch_prefill_combine(const PrefillParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_pieces, 128 / kCombineWarps);
+    cfg.gridDim = dim3(p.n_pieces, 128 / kCombineWarps, p.mode == 2 ? 1 : 2);
     cfg.blockDim = dim3(kCombineWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
