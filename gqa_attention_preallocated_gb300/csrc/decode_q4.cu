@@ -32,11 +32,12 @@
 //    on distinct shared-memory banks and V's at most two to a bank (d = 128).
 //
 // Range.  q is scaled by a power of two to just below 2^15 a row, so that f16
-// holds it exactly whatever its size.  Weights are f16 too: p s_v 2^(133 - e),
+// holds it exactly whatever its size (below 2^112, where the factor that undoes
+// it leaves fp32).  Weights are f16 too: p s_v 2^(133 - e),
 // e the largest step exponent met so far (moved, with O, when a larger one
 // appears), below 2^16 as p is below 2^8 (the reference maximum moves only
-// past that) and s_v 2^(127 - e) below 2.  f16 keeps 11 bits of a weight; the
-// zero point's sum uses the rounded weights, so the rounding acts on
+// past that) and s_v 2^(127 - e) below 2.  f16 keeps 11 bits of a weight, or
+// 2^-31 of the largest step where that is more; the zero point's sum uses the rounded weights, so the rounding acts on
 // c - z and not on c.  Sums, maxima, l and O are fp32.
 //
 // Rows that a query must not see may hold anything: their scores, steps and
@@ -81,6 +82,7 @@ struct Q4Shape {
     static constexpr bool kQSmem = QB > 2;  // query fragments in shared memory, not in registers
     static constexpr size_t kQbuf = kQSmem ? QB * (D / 32) * 32 * 16 : 0;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + kQbuf + 2 * kStages * 8 + 16;
+    static_assert(kStages >= 2 * kGroups, "a stage to read and one to fill for every group");
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -180,36 +182,35 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
         // Query fragments: this thread holds query row g's dims quad * D / 4 ..,
         // word by word; the k-steps of a word take its value pairs (0, 1), (2, 3)
         // and (4, 5), (6, 7), whose codes come as c 2^-24 and c 2^-20 in turn.
-        // All rows are scaled by one power of two, 2^(141 - e), e the exponent
-        // field of the largest |q|.
+        // Each row is scaled by a power of two, 2^(141 - e), e the exponent field of
+        // its largest |q|.
         uint4 qa[QB][KW];  // (in shared memory with many rows)
         float qs[QB][2];   // sums of the scaled q of query rows 8 nb + 2 quad, + 1, times 2^-24
-        float rs;          // scores' factor: 2^(e - 141) 2^24 log2(e) / sqrt(d)
+        float rs[QB][2];   // their scores' factor: 2^(e - 141) 2^24 log2(e) / sqrt(d)
         {
-            uint4 w[QB][KW];
-            uint32_t top = 0;
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb) {
                 const uint4* qrow = nullptr;
                 if ((valid >> (nb * 8 + g)) & 1u)
                     qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + nb * 8 + g) * D + quad * (D / 4));
+                uint4 w[KW];
+                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < KW; ++i) {
-                    w[nb][i] = qrow ? __ldg(qrow + i) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t u[4] = {w[nb][i].x, w[nb][i].y, w[nb][i].z, w[nb][i].w};
+                    w[i] = qrow ? __ldg(qrow + i) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) top = max(top, max(u[c] & 0x7FFFu, (u[c] >> 16) & 0x7FFFu));
                 }
-            }
-            const int e = max(14, static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7));
-            const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-            rs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23);
-#pragma unroll
-            for (int nb = 0; nb < QB; ++nb) {
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = max(14, static_cast<int>(top >> 7));
+                const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+                const float rowf = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23);
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < KW; ++i) {
-                    const uint32_t u[4] = {w[nb][i].x, w[nb][i].y, w[nb][i].z, w[nb][i].w};
+                    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
                     uint32_t hq[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -228,6 +229,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     qs[nb][h] = __shfl_sync(0xffffffffu, sum, (2 * quad + h) * 4) * 5.9604644775390625e-8f;  // 2^-24
+                    rs[nb][h] = __shfl_sync(0xffffffffu, rowf, (2 * quad + h) * 4);
                 }
             }
         }
@@ -321,13 +323,13 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t ex = vw[kb][h] >> 23;
                     ve = max(ve, ex == 255u ? 0u : ex);  // (a NaN step stays NaN under any factor)
-                    const float ks = q4::step_of(kw[kb][h]) * rs, kz = -small_to_f32(kw[kb][h] & 0xFFFFu);
+                    const float ks = q4::step_of(kw[kb][h]), kz = -small_to_f32(kw[kb][h] & 0xFFFFu);
 #pragma unroll
                     for (int nb = 0; nb < QB; ++nb)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             float& v = sc[kb][nb][2 * h + c];
-                            v = fmaf(fmaf(kz, qs[nb][c], v), ks, nm[nb][c]);
+                            v = fmaf(fmaf(kz, qs[nb][c], v), ks * rs[nb][c], nm[nb][c]);
                         }
                 }
             }

@@ -45,7 +45,7 @@ struct WideShape {
     static constexpr int kPS = D + 4;                 // floats of a partial's row: O, m, l, pad
     static constexpr int kPRow = kKT * 2 + 16;        // bytes of a weight row (the pad spreads 8 rows over all banks)
     // Behind the stages: states [group][key half][row][kPS], weights [group][2][row],
-    // query fragments [QB][4 words][32 lanes] of 16 bytes, sums of q [row], each
+    // query fragments [QB][4 words][32 lanes] of 16 bytes, (sum of q, score factor) [row], each
     // warp's maxima [group][warp][row] and exponents, sums l and zero points'
     // [group][warp][row], references of a group [group][row], sums set aside
     // [block][thread].
@@ -54,12 +54,13 @@ struct WideShape {
     static constexpr int kPbuf = kGroups * 2 * kPhalf;
     static constexpr int kSave = QB * kCT * 16;       // l and zero points' sums set aside, 16 bytes a thread and block
     static constexpr int kQbuf = QB * 4 * 32 * 16;
-    static constexpr int kOffP = kObuf, kOffQ = kOffP + kPbuf, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 4,
+    static constexpr int kOffP = kObuf, kOffQ = kOffP + kPbuf, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 8,
                          kOffVe = kOffMx + kCW * kRows * 4, kOffLz = kOffVe + 64, kOffM = kOffLz + kCW * kRows * 8,
                          kOffSave = kOffM + kGroups * kRows * 4, kMisc = kOffSave + kSave;
     static constexpr int kFit = (232448 - 1024 - 512 - kMisc) / kStageB;
     static constexpr int kStages = kFit / kGroups * kGroups;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kMisc + 2 * kStages * 8 + 16;
+    static_assert(kStages >= 2 * kGroups, "a stage to read and one to fill for every group");
     static_assert(kSmem <= 232448 && kMisc % 16 == 0 && kOffQ % 16 == 0 && kOffP % 16 == 0 && kOffLz % 8 == 0 && kOffSave % 16 == 0, "shared memory map");
 };
 
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     const uint32_t pbuf = misc0 + S::kOffP + grp * 2 * S::kPhalf;
     const uint32_t pstore = pbuf + g * S::kPRow + (2 * quad) * 2;  // + half, + block of rows, + key
     const uint32_t pload = pbuf + (lane & 7) * S::kPRow + (kh * 64 + (lane >> 3) * 8) * 2;
-    float* qsum = reinterpret_cast<float*>(misc + S::kOffQs);
+    float2* qsum = reinterpret_cast<float2*>(misc + S::kOffQs);
     float* mxbuf = reinterpret_cast<float*>(misc + S::kOffMx) + grp * kTileWarps * S::kRows;
     uint32_t* vebuf = reinterpret_cast<uint32_t*>(misc + S::kOffVe) + grp * kTileWarps;
     float2* lzbuf = reinterpret_cast<float2*>(misc + S::kOffLz);
@@ -166,18 +167,15 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
         }
         const uint32_t valid = __ballot_sync(0xffffffffu, lane_lim >= 0);
 
-        // Query fragments (as in decode_q4.cu), written by warp nb for block nb;
-        // every warp reads all rows for the common exponent.
-        float rs;
+        // Query fragments (as in decode_q4.cu): warp nb writes block nb's, and its
+        // rows' sums and score factors.
         {
-            uint32_t top = 0;
-            uint4 w[4];
-#pragma unroll
-            for (int nb = QB - 1; nb >= 0; --nb) {  // (ends with the warp's own block in w)
-                const int blk = (warp + 1 + nb) % QB;
+            if (warp < QB) {
                 const uint4* qrow = nullptr;
-                if ((valid >> (blk * 8 + g)) & 1u)
-                    qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + blk * 8 + g) * D + quad * 32);
+                if ((valid >> (warp * 8 + g)) & 1u)
+                    qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + warp * 8 + g) * D + quad * 32);
+                uint4 w[4];
+                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     w[i] = qrow ? __ldg(qrow + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -185,12 +183,10 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) top = max(top, max(u[c] & 0x7FFFu, (u[c] >> 16) & 0x7FFFu));
                 }
-            }
-            const int e = max(14, static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 7));
-            const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
-            rs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23);  // 2^(e - 141) 2^24
-            const int blk = (warp + 1) % QB;  // the block left in w
-            if (warp < QB) {
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = max(14, static_cast<int>(top >> 7));
+                const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -203,11 +199,13 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                         const float t = (c & 1) ? 0.0625f : 1.f;
                         h[c] = ptx::pack_f16x2(a0 * t, a1 * t);
                     }
-                    *reinterpret_cast<uint4*>(misc + S::kOffQ + ((blk * 4 + i) * 32 + lane) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(misc + S::kOffQ + ((warp * 4 + i) * 32 + lane) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if (quad == 0) qsum[blk * 8 + g] = sum * 5.9604644775390625e-8f;  // 2^-24
+                if (quad == 0)  // 2^-24 sum, and 2^(e - 141) 2^24 log2(e) / sqrt(d)
+                    qsum[warp * 8 + g] = make_float2(sum * 5.9604644775390625e-8f,
+                                                     p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23));
             }
             ptx::named_barrier_sync(1, S::kCT);
         }
@@ -271,15 +269,15 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                     if (key >= extent || key <= min_lo) kw[h] = vw[h] = 0u;
                 }
             }
-            const float ks0 = step_of(kw[0]) * rs, ks1 = step_of(kw[1]) * rs;
+            const float ks0 = step_of(kw[0]), ks1 = step_of(kw[1]);
             const float kz0 = -small_to_f32(kw[0] & 0xFFFFu), kz1 = -small_to_f32(kw[1] & 0xFFFFu);
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb) {
-                const float2 qs = *reinterpret_cast<const float2*>(qsum + nb * 8 + 2 * quad);
-                sc[nb][0] = fmaf(fmaf(kz0, qs.x, sc[nb][0]), ks0, nm[nb][0]);
-                sc[nb][1] = fmaf(fmaf(kz0, qs.y, sc[nb][1]), ks0, nm[nb][1]);
-                sc[nb][2] = fmaf(fmaf(kz1, qs.x, sc[nb][2]), ks1, nm[nb][0]);
-                sc[nb][3] = fmaf(fmaf(kz1, qs.y, sc[nb][3]), ks1, nm[nb][1]);
+                const float4 qs = *reinterpret_cast<const float4*>(qsum + nb * 8 + 2 * quad);  // of two rows
+                sc[nb][0] = fmaf(fmaf(kz0, qs.x, sc[nb][0]), ks0 * qs.y, nm[nb][0]);
+                sc[nb][1] = fmaf(fmaf(kz0, qs.z, sc[nb][1]), ks0 * qs.w, nm[nb][1]);
+                sc[nb][2] = fmaf(fmaf(kz1, qs.x, sc[nb][2]), ks1 * qs.y, nm[nb][0]);
+                sc[nb][3] = fmaf(fmaf(kz1, qs.z, sc[nb][3]), ks1 * qs.w, nm[nb][1]);
             }
             if (!full) {
 #pragma unroll

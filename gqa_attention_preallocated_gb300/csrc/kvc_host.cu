@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <queue>
@@ -1014,7 +1015,7 @@ static kvc_status create_impl(kvc_cache** out, int layers, int batch, int kv_hea
                 return fail(KVC_ERR_ARG, "layer %d scale buffer not 16-byte aligned", l);
         }
     }
-    kvc_cache* c = new kvc_cache;
+    std::unique_ptr<kvc_cache> c(new kvc_cache);  // (the vectors below may throw)
     c->layers = layers;
     c->B = batch;
     c->Hkv = kv_heads;
@@ -1036,7 +1037,7 @@ static kvc_status create_impl(kvc_cache** out, int layers, int batch, int kv_hea
     c->tm_ready.assign(layers, 0);
     c->kscale.assign(static_cast<size_t>(layers) * kv_heads, 1.0f);
     c->vscale.assign(static_cast<size_t>(layers) * kv_heads, 1.0f);
-    *out = c;
+    *out = c.release();
     return ok();
 }
 

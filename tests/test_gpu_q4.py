@@ -391,6 +391,30 @@ def test_nan_rows_reach_their_queries_only():
         assert bad[:, 1].all() and not bad[:, 0].any() and not bad[:, 2].any()
 
 
+@pytest.mark.parametrize("d,T", [(64, 1), (128, 1), (128, 4), (64, 4), (96, 2), (128, 20)])
+def test_queries_of_very_different_size_and_nan_queries(d, T):
+    """Heads and tokens whose queries differ by 2^60 each keep their precision; a NaN or infinite query is NaN alone."""
+    p = Pair(2, 2, d, 200, seed=d + T)
+    p.step([150, 90], 4)
+    q, k, v = p.inputs([T, T], T, 4)
+    size = torch.tensor(2.0) ** torch.tensor([0.0, -40.0, 3.0, -60.0])
+    q = _bf(q.double() * size.double().repeat(2)[None, :, None, None])
+    p.c.append(0, k.cuda(), v.cuda(), [T, T])
+    p.note(k, v, [T, T])
+    out = p.c.gqa_attention(0, q.cuda(), [T, T])
+    p.check_out(out, q, [T, T], T)
+    bad = q.clone()
+    bad[0, 1, 0, 5], bad[1, 6, T - 1, 0] = math.nan, math.inf
+    got = p.c.gqa_attention(0, bad.cuda(), [T, T])
+    lost = torch.isnan(got).all(-1).cpu()
+    assert lost[0, 1, 0] and lost[1, 6, T - 1]
+    lost[0, 1, 0] = lost[1, 6, T - 1] = False
+    assert not lost.any()
+    keep = torch.ones_like(lost)
+    keep[0, 1, 0] = keep[1, 6, T - 1] = False
+    assert torch.equal(got.cpu()[keep], out.cpu()[keep])
+
+
 def test_layers_truncate_and_host_buffers():
     p = Pair(2, 2, 128, 256, layers=2, layer=1, seed=2)
     p.step([70, 33], 4)
@@ -463,7 +487,7 @@ def test_device_steps_and_graph(d, G, page, T):
 def test_allocation_free_call(d):
     p = Pair(3, 2, d, 300, seed=d)
     p.step([100, 1, 260], 4)
-    for T in (1, 4):
+    for T in (1, 4, 30):
         q, k, v = p.inputs([T, 0, T], T, 4)
         p.c.append(0, k.cuda(), v.cuda(), [T, 0, T])
         p.note(k, v, [T, 0, T])
