@@ -81,7 +81,7 @@ struct Q4Shape {
     static constexpr int kStages = (kFit < 20 ? kFit : 20) / kGroups * kGroups;
     static constexpr bool kQSmem = QB > 2;  // query fragments in shared memory, not in registers
     static constexpr size_t kQbuf = kQSmem ? QB * (D / 32) * 32 * 16 : 0;
-    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + kQbuf + 2 * kStages * 8 + 16;
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + kQbuf + 2 * kStages * 8 + 16 + sizeof(Segment);
     static_assert(kStages >= 2 * kGroups, "a stage to read and one to fill for every group");
     static_assert(kSmem <= 232448, "shared memory per CTA");
 };
@@ -107,11 +107,12 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     const uint32_t qfrag = ptx::smem_addr(qbuf);
     uint64_t* bars = reinterpret_cast<uint64_t*>(qbuf + S::kQbuf);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages);
+    volatile Segment* seg = reinterpret_cast<volatile Segment*>(bars + 2 * kStages + 2);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Part<DP> wp{p};
     long long N = DP ? 0 : wp.total_tiles();
-    const long long P = gridDim.x;
+    long long P = gridDim.x;
     int x0 = static_cast<int>(static_cast<long long>(blockIdx.x) * N / P);
     int x1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * N / P);
 
@@ -131,8 +132,12 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     if (DP) {
         if (p.dplan->skip) return;  // a rejected device-resident step: nothing is written
         N = wp.total_tiles();
-        x0 = static_cast<int>(static_cast<long long>(blockIdx.x) * N / P);
-        x1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * N / P);
+        // (With the counters every CTA of a unit's range must have a tile: no more
+        // CTAs than tiles, as the host's plan has it.)
+        if (p.counters) P = min(P, max(N, 1ll));
+        const long long i = min(static_cast<long long>(blockIdx.x), P);
+        x0 = static_cast<int>(i * N / P);
+        x1 = static_cast<int>(min(i + 1, P) * N / P);
     }
 
     zero_padded_queries<D, DP>(p, wp, tid, S::kThreads);
@@ -171,6 +176,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
         const int seg_key0 = (cur.t0 + j0) * kKT + koff - (x - x0) * kKT;  // + it * kKT: the slice's first key
         // Query row i of the block is row row0 + i of q and out (packed g * T + t);
         // lane i holds its last visible key (-1: no such query), `valid` has its bit.
+        // (Kept in shared memory for the segment's end: registers are short.)
         const size_t row0 = (static_cast<size_t>(b) * p.Hq + kvh * p.G) * p.T + rb * p.RPB;
         int lane_lim;
         {
@@ -178,6 +184,12 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             lane_lim = (lane < S::kRows && r < p.R && t < nn) ? prior + t : -1;
         }
         const uint32_t valid = __ballot_sync(0xffffffffu, lane_lim >= 0);
+        if (tid == 0) {
+            seg->row0 = row0;
+            seg->valid = valid;
+            seg->unit_tile = x - j0;
+            seg->unit = cur.q * p.Hkv + kvh;
+        }
 
         // Query fragments: this thread holds query row g's dims quad * D / 4 ..,
         // word by word; the k-steps of a word take its value pairs (0, 1), (2, 3)
@@ -531,11 +543,14 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             ptx::named_barrier_sync(1, S::kCT);
             // Merge them in the order of the warps, and write the unit's output
             // (this CTA saw all of it) or the CTA's partial.
+            const size_t out_row0 = seg->row0;
+            const uint32_t out_valid = seg->valid;
+            const int unit = seg->unit;
             const bool sole = nseg == cur.nt;
             constexpr int C4 = D / 4;
             for (int idx = tid; idx < S::kRows * C4; idx += S::kCT) {
                 const int lr = idx / C4, c4 = idx - lr * C4;
-                if (!((valid >> lr) & 1u)) continue;
+                if (!((out_valid >> lr) & 1u)) continue;
                 const float* st = obuf + lr * PS;
                 float M = -INFINITY;
 #pragma unroll
@@ -554,8 +569,10 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     acc.z = fmaf(v.z, f, acc.z);
                     acc.w = fmaf(v.w, f, acc.w);
                 }
-                write_row<D>(p, row0 + lr, c4, acc, M, L, sole, cur.q * p.Hkv + kvh + blockIdx.x, lr);
+                write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + blockIdx.x, lr);
             }
+            if (!sole && p.counters)
+                finish_unit<D, S::kRows>(p, unit, seg->unit_tile, cur.nt, N, P, out_row0, out_valid, tid, S::kCT, seg->flag);
             ptx::named_barrier_sync(1, S::kCT);
         }
         x += nseg;

@@ -382,6 +382,11 @@ Q4Scales q4_scales(const kvc_cache* c, int layer) {
     return s;
 }
 
+// The workspace's counters of a 4-bit call's units, when it has enough of them.
+int* unit_counters(const kvc_cache* c, const AttnPlan& pl, uint8_t* ws) {
+    return c->dtype == KVC_Q4 && pl.units <= kWsCounters ? reinterpret_cast<int*>(ws + kWsCounterOffset) : nullptr;
+}
+
 // The layer's FP8 scales into a split-KV parameter block (no-op for bf16).
 void set_decode_scales(const kvc_cache* c, int layer, DecodeParams* p) {
     if (c->dtype != KVC_FP8_E4M3) return;
@@ -715,6 +720,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     p.pg = c->pg;
     set_decode_scales(c, layer, &p);
     p.q4 = q4_scales(c, layer);
+    p.counters = unit_counters(c, pl, wsb);
     p.anc = nullptr;
     if (anc) {
         // The masks go to the workspace (the parameter block stays small).
@@ -774,7 +780,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     // floor(iN/P) .. floor((i+1)N/P)-1, so tile x belongs to CTA
     // ((x+1)P - 1) / N) and, when warps own whole tiles, it is one tile.
     bool need_combine = false;
-    {
+    if (!p.counters) {
         const long long N = tiles, P = grid;
         for (int q = 0; q < pl.NB && !need_combine; ++q) {
             const int nt = (p.gstart[q + 1] - p.gstart[q]) / c->Hkv;
@@ -1674,10 +1680,12 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     p.pg = c->pg;
     set_decode_scales(c, layer, &p);
     p.q4 = q4_scales(c, layer);
+    p.counters = unit_counters(c, pl, wsb);
     e = c->dtype == KVC_Q4 ? launch_decode_q4(p, grid, c->d, st)
                            : launch_decode_bf16(p, c->tmK[layer], c->tmV[layer], 1, grid, c->dtype == KVC_FP8_E4M3, c->d, st);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV attention launch");
     ++c->launches;
+    if (p.counters) return ok();  // (the attention kernel merges its units)
 
     static_assert(sizeof(CombineParams) < 32000, "kernel parameter block too large");
     CombineParams cp{};

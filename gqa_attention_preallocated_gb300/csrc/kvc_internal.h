@@ -184,6 +184,9 @@ struct DecodeParams {
     float kscale[kMaxScaleHeads];
     float vscale[kMaxScaleHeads];
     Q4Scales q4;             // 4-bit cache: the rows' scale words
+    // 4-bit caches: an arrival counter a unit (zero between calls), with which
+    // the last CTA of a unit merges its partials; null: the combine kernel does.
+    int* counters;
     int prior[kMaxBatch];    // lens[b] - n_new[b]
     int n_new[kMaxBatch];
     int gstart[kMaxGroups + 1];
@@ -282,7 +285,8 @@ constexpr int kMaxPrefillSlots = 4095;  // key-split pieces per launch (each has
 // Workspace header: the error word, then one merge counter per (first slot of
 // a split block, head); the partials follow the header.
 constexpr size_t kWsCounterOffset = 256;
-constexpr size_t kWsHeaderBytes = kWsCounterOffset + static_cast<size_t>(kMaxPrefillSlots + 1) * 2 * sizeof(int);
+constexpr int kWsCounters = (kMaxPrefillSlots + 1) * 2;
+constexpr size_t kWsHeaderBytes = kWsCounterOffset + static_cast<size_t>(kWsCounters) * sizeof(int);
 struct PrefillParams {
     const void* q;
     void* out;

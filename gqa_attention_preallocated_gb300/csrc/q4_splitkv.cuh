@@ -29,6 +29,16 @@ struct Stage {
     static constexpr int kBytes = 2 * kCodeB + 2 * kKT * 4;
 };
 
+// What a segment's end needs of its beginning (in shared memory).
+struct Segment {
+    unsigned long long row0;  // first query row of the block in q and out
+    int flag[2];              // finish_unit's
+    uint32_t valid;           // the block's rows that are queries
+    int unit, unit_tile;      // the unit and its first tile
+    int pad;
+};
+static_assert(sizeof(Segment) == 32, "shared memory map");
+
 // Key of row i (0 .. 7) of an 8-key block, a nibble each.
 template <int D>
 __device__ __forceinline__ int perm8(int i) {
@@ -114,6 +124,70 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, size_t row, int
     if (c4 == 0) {
         part[D] = M;
         part[D + 1] = L;
+    }
+}
+
+// The end of a unit of which this CTA saw a part: the last CTA to leave its
+// partial merges all of them, in the order of the CTAs, and writes the unit's
+// output.  Called by all `threads` consumer threads, after the partial's writes;
+// `flag` is two ints of shared memory.  unit = (group q, KV head kvh), us its
+// first tile of N, ntiles its tiles; P CTAs.  p.counters returns to zero.
+template <int D, int kRows>
+__device__ __forceinline__ void finish_unit(const DecodeParams& p, int unit, long long us, int ntiles, long long N, long long P,
+                                            size_t row0, uint32_t valid, int tid, int threads, volatile int* flag) {
+    constexpr int PS = D + 4, C4 = D / 4, kChunk = 8;
+    __threadfence();
+    ptx::named_barrier_sync(1, threads);
+    if (tid == 0) {
+        // Tile x belongs to CTA ((x + 1) P - 1) / N.
+        const int c0 = static_cast<int>(((us + 1) * P - 1) / N), c1 = static_cast<int>(((us + ntiles) * P - 1) / N);
+        const bool last = atomicAdd(p.counters + unit, 1) == c1 - c0;
+        flag[0] = last ? c1 - c0 + 1 : 0;
+        flag[1] = c0;
+        if (last) p.counters[unit] = 0;  // ready for the next call
+    }
+    ptx::named_barrier_sync(1, threads);
+    const int n = flag[0];
+    if (n > 0) {
+        __threadfence();
+        const float* base = p.partials + static_cast<size_t>(unit + flag[1]) * p.part_rows * PS;
+        const size_t step = static_cast<size_t>(p.part_rows) * PS;
+        for (int idx = tid; idx < kRows * C4; idx += threads) {
+            const int lr = idx / C4, c4 = idx - lr * C4;
+            if (!((valid >> lr) & 1u)) continue;
+            const float* row = base + static_cast<size_t>(lr) * PS;
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < n; k0 += kChunk) {
+                float2 ml[kChunk];
+                float4 o[kChunk];
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) {
+                    const float* part = row + (k0 + k < n ? k0 + k : k0) * step;
+                    ml[k] = __ldcg(reinterpret_cast<const float2*>(part + D));
+                    o[k] = __ldcg(reinterpret_cast<const float4*>(part) + c4);
+                    if (k0 + k >= n) ml[k] = make_float2(-INFINITY, 0.f);
+                }
+                const float old = M;
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) M = fmaxf(M, ml[k].x);
+                const float Mu = M == -INFINITY ? 0.f : M;
+                const float f = ptx::ex2(old - Mu);  // (0 before the first)
+                L *= f;
+                acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) {
+                    if (k0 + k >= n) break;
+                    const float w = ptx::ex2(ml[k].x - Mu);
+                    L = fmaf(w, ml[k].y, L);
+                    acc.x = fmaf(w, o[k].x, acc.x);
+                    acc.y = fmaf(w, o[k].y, acc.y);
+                    acc.z = fmaf(w, o[k].z, acc.z);
+                    acc.w = fmaf(w, o[k].w, acc.w);
+                }
+            }
+            write_row<D>(p, row0 + lr, c4, acc, M, L, true, 0, lr);
+        }
     }
 }
 
