@@ -8,8 +8,8 @@
 //   score = s_k (raw - z_k sum(q)) / sqrt(d)
 //   out   = sum_k p_k s_v (c_k - z_v) / sum_k p_k
 // so no single value is ever rescaled: K's step and zero point act on a score,
-// V's step joins the softmax weight, and V's zero point is one running sum a
-// query row.
+// V's step joins the softmax weight, and V's zero points are one more dimension
+// of the output, which is taken from all the others at the end.
 //
 // Codes as matrix operands.  A 4-bit integer in the low bits of an f16 is the
 // subnormal c 2^-24, exactly, and at bits 4 .. 7 it is c 2^-20; the tensor core
@@ -37,8 +37,11 @@
 // e the largest step exponent met so far (moved, with O, when a larger one
 // appears), below 2^16 as p is below 2^8 (the reference maximum moves only
 // past that) and s_v 2^(127 - e) below 2.  f16 keeps 11 bits of a weight, or
-// 2^-31 of the largest step where that is more; the zero point's sum uses the rounded weights, so the rounding acts on
-// c - z and not on c.  Sums, maxima, l and O are fp32.
+// 2^-31 of the largest step where that is more.  The zero points' sum runs
+// through the same products as the codes' (their f16 pairs as one more row of
+// V^T), so that the weights' rounding acts on c - z, and the tensor core's
+// truncation, 2^-23 of a sum each time it adds, on both alike: over 131072 keys
+// the two sums are some 300 times their difference.  Maxima, l and O are fp32.
 //
 // Rows that a query must not see may hold anything: their scores, steps and
 // weights are replaced, never multiplied.  Codes cannot be NaN, so V needs no
@@ -251,8 +254,9 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
         // The segment's state.
         float o[QB][MB][4];
         // Rows' reference (and its negative, 0 before the first key; a row that is
-        // no query keeps reference 0), sums of p, of p s_v z_v.
-        float m[QB][2], nm[QB][2], l[QB][2], zs[QB][2];
+        // no query keeps reference 0), sums of p; of p s_v z_v (the accumulator of
+        // 16 equal rows).
+        float m[QB][2], nm[QB][2], l[QB][2], zs[QB][4];
         bool fresh = true;                                // some query of the block has met no key yet
         uint32_t vexp = kMinExp;                          // exponent field of the largest V step met (at least kMinExp)
         float vmul = __uint_as_float((260u - kMinExp) << 23);  // 2^(133 - vexp)
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 m[nb][h] = ((valid >> (nb * 8 + 2 * quad + h)) & 1u) ? -INFINITY : 0.f;
-                nm[nb][h] = l[nb][h] = zs[nb][h] = 0.f;
+                nm[nb][h] = l[nb][h] = zs[nb][h] = zs[nb][2 + h] = 0.f;
             }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) o[nb][mb][0] = o[nb][mb][1] = o[nb][mb][2] = o[nb][mb][3] = 0.f;
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t ex = vw[kb][h] >> 23;
                     ve = max(ve, ex == 255u ? 0u : ex);  // (a NaN step stays NaN under any factor)
-                    const float ks = q4::step_of(kw[kb][h]), kz = -small_to_f32(kw[kb][h] & 0xFFFFu);
+                    const float ks = q4::step_of(kw[kb][h]), kz = -zero_f32(kw[kb][h]);
 #pragma unroll
                     for (int nb = 0; nb < QB; ++nb)
 #pragma unroll
@@ -403,6 +407,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                         l[nb][c] *= f[c];
                         f[c] *= fv;
                         zs[nb][c] *= f[c];
+                        zs[nb][2 + c] *= f[c];
                     }
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb) {
@@ -415,10 +420,8 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             }
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                // Weights: p into l, p s_v (f16) into the products, times z_v into
-                // the zero points' sum.
+                // Weights: p into l, p s_v (f16) into the products.
                 const float vs0 = q4::step_of(vw[kb][0]) * vmul, vs1 = q4::step_of(vw[kb][1]) * vmul;
-                const float vz0 = small_to_f32(vw[kb][0] & 0xFFFFu), vz1 = small_to_f32(vw[kb][1] & 0xFFFFu);
                 uint32_t pb[QB][2];
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
@@ -435,13 +438,18 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                             if (sc[kb][nb][e] == -INFINITY) pw[e] = 0.f;  // (a NaN step that this query does not see)
                     }
                     const uint32_t h0 = ptx::pack_f16x2(pw[0], pw[1]), h1 = ptx::pack_f16x2(pw[2], pw[3]);
-                    const float2 r0 = f16x2_to_f32(h0), r1 = f16x2_to_f32(h1);
-                    zs[nb][0] = fmaf(r1.x, vz1, fmaf(r0.x, vz0, zs[nb][0]));
-                    zs[nb][1] = fmaf(r1.y, vz1, fmaf(r0.y, vz0, zs[nb][1]));
                     pb[nb][0] = transpose8x8(h0);
                     pb[nb][1] = transpose8x8(h1);
                 }
-                // O^T += V^T P^T.
+                // O^T += V^T P^T, and the zero points'.
+                {
+                    // (Accumulator row g's key has its zero point here; the transpose
+                    // gives each thread those of its k index's keys.)
+                    const uint32_t z0 = transpose8x8(zero_pair(vw[kb][0], vw[kb][0])), z8 = transpose8x8(zero_pair(vw[kb][1], vw[kb][1]));
+                    const uint32_t a[4] = {z0, z0, z8, z8};
+#pragma unroll
+                    for (int nb = 0; nb < QB; ++nb) ptx::mma_f16_16816(zs[nb], a, pb[nb][0], pb[nb][1]);
+                }
                 uint32_t va0[VW], vb0[VW], va8[VW], vb8[VW];
                 const uint32_t pa = sV + vpiece_a + (at + kb * 16) * S::kRowB, pc = sV + vpiece_b + (at + kb * 16) * S::kRowB;
                 if constexpr (D == 128) {
@@ -514,7 +522,6 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) {
                         l[nb][h] += __shfl_xor_sync(0xffffffffu, l[nb][h], d);
-                        zs[nb][h] += __shfl_xor_sync(0xffffffffu, zs[nb][h], d);
                     }
                     // A row whose every score is NaN keeps that through the merges.
                     if (m[nb][h] == -INFINITY && l[nb][h] != 0.f) m[nb][h] = 0.f;
@@ -528,8 +535,8 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const int v = (c & 1) * 4 + (c >> 1);
-                            e[v] = fmaf(o[nb][4 * i + c][h], 16777216.f, -zs[nb][h]) * 0.015625f * real;
-                            e[v + 2] = fmaf(o[nb][4 * i + c][2 + h], 1048576.f, -zs[nb][h]) * 0.015625f * real;
+                            e[v] = (o[nb][4 * i + c][h] - zs[nb][h]) * 262144.f * real;  // 2^24 2^-6
+                            e[v + 2] = fmaf(o[nb][4 * i + c][2 + h], 0.0625f, -zs[nb][h]) * 262144.f * real;
                         }
                         float4* d4 = reinterpret_cast<float4*>(st + g * (D / 8) + i * 8);
                         d4[0] = make_float4(e[0], e[1], e[2], e[3]);

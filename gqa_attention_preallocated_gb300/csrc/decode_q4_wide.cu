@@ -16,10 +16,10 @@
 // tile, also ORs the warps' findings that they do not, and then the four redo
 // the tile's scores with references moved together (the first tile of a unit,
 // and rarely after it: a maximum has to pass the reference by 2^8).  For that
-// the sums l and of the zero points are set aside in shared memory before each
-// tile.  The weights' buffer is double, so that the next tile's may be written
-// while a slower warp still reads.  Two or three such groups take tiles in turn
-// and hide each other's barriers.
+// the sums l are set aside in shared memory before each tile.  The weights'
+// buffer is double, so that the next tile's may be written while a slower warp
+// still reads.  Two or three such groups take tiles in turn and hide each
+// other's barriers.
 // The queries' fragments live in shared memory: they would be 16 registers a
 // block of 8 rows.
 
@@ -46,13 +46,13 @@ struct WideShape {
     static constexpr int kPRow = kKT * 2 + 16;        // bytes of a weight row (the pad spreads 8 rows over all banks)
     // Behind the stages: states [group][key half][row][kPS], weights [group][2][row],
     // query fragments [QB][4 words][32 lanes] of 16 bytes, (sum of q, score factor) [row], each
-    // warp's maxima [group][warp][row] and exponents, sums l and zero points'
+    // warp's maxima [group][warp][row] and exponents, sums l and the zero points'
     // [group][warp][row], references of a group [group][row], sums set aside
     // [block][thread].
     static constexpr int kObuf = kGroups * 2 * kRows * kPS * 4;
     static constexpr int kPhalf = kRows * kPRow;      // one tile's weights of a group; two of them
     static constexpr int kPbuf = kGroups * 2 * kPhalf;
-    static constexpr int kSave = QB * kCT * 16;       // l and zero points' sums set aside, 16 bytes a thread and block
+    static constexpr int kSave = QB * kCT * 8;        // l set aside, 8 bytes a thread and block
     static constexpr int kQbuf = QB * 4 * 32 * 16;
     static constexpr int kOffP = kObuf, kOffQ = kOffP + kPbuf, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 8,
                          kOffVe = kOffMx + kCW * kRows * 4, kOffLz = kOffVe + 64, kOffM = kOffLz + kCW * kRows * 8,
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     uint32_t* vebuf = reinterpret_cast<uint32_t*>(misc + S::kOffVe) + grp * kTileWarps;
     float2* lzbuf = reinterpret_cast<float2*>(misc + S::kOffLz);
     float* mbuf = reinterpret_cast<float*>(misc + S::kOffM);
-    float4* save = reinterpret_cast<float4*>(misc + S::kOffSave) + tid;
+    float2* save = reinterpret_cast<float2*>(misc + S::kOffSave) + tid;
 
     Cursor<DP, kKT> cur;
     cur.init(wp, x0);
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
         // the group's references (0 before a row's first key; `seen` has a bit for
         // each row that has one, or is no query); sums over this warp's scored keys.
         float o[QB][4][4];
-        float nm[QB][2], l[QB][2], zs[QB][2];
+        float nm[QB][2], l[QB][2], zs[QB][4];
         uint32_t seen = 0;
         uint32_t vexp = kMinExp;
         float vmul = __uint_as_float((260u - kMinExp) << 23);  // 2^(133 - vexp)
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 if (!((valid >> (nb * 8 + 2 * quad + c)) & 1u)) seen |= 1u << (2 * nb + c);
-                nm[nb][c] = l[nb][c] = zs[nb][c] = 0.f;
+                nm[nb][c] = l[nb][c] = zs[nb][c] = zs[nb][2 + c] = 0.f;
             }
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb) o[nb][mb][0] = o[nb][mb][1] = o[nb][mb][2] = o[nb][mb][3] = 0.f;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 }
             }
             const float ks0 = step_of(kw[0]), ks1 = step_of(kw[1]);
-            const float kz0 = -small_to_f32(kw[0] & 0xFFFFu), kz1 = -small_to_f32(kw[1] & 0xFFFFu);
+            const float kz0 = -zero_f32(kw[0]), kz1 = -zero_f32(kw[1]);
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb) {
                 const float4 qs = *reinterpret_cast<const float4*>(qsum + nb * 8 + 2 * quad);  // of two rows
@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
             // (a NaN step has no exponent: it stays NaN under any factor)
             ve = max(ve, max((vw[0] >> 23) == 255u ? 0u : vw[0] >> 23, (vw[1] >> 23) == 255u ? 0u : vw[1] >> 23));
             const float vs0 = step_of(vw[0]) * vmul, vs1 = step_of(vw[1]) * vmul;
-            const float vz0 = small_to_f32(vw[0] & 0xFFFFu), vz1 = small_to_f32(vw[1] & 0xFFFFu);
 #pragma unroll
             for (int nb = 0; nb < QB; ++nb) {
                 float pw[4];
@@ -327,9 +326,6 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                         if (sc[nb][e] == -INFINITY) pw[e] = 0.f;  // (a NaN step that this query does not see)
                 }
                 const uint32_t h0 = ptx::pack_f16x2(pw[0], pw[1]), h1 = ptx::pack_f16x2(pw[2], pw[3]);
-                const float2 r0 = f16x2_to_f32(h0), r1 = f16x2_to_f32(h1);
-                zs[nb][0] = fmaf(r1.x, vz1, fmaf(r0.x, vz0, zs[nb][0]));
-                zs[nb][1] = fmaf(r1.y, vz1, fmaf(r0.y, vz0, zs[nb][1]));
                 const uint32_t to = pst + nb * 8 * S::kPRow;
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(transpose8x8(h0)) : "memory");
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 16), "r"(transpose8x8(h1)) : "memory");
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 
             bool moved = false;
 #pragma unroll
-            for (int nb = 0; nb < QB; ++nb) save[nb * S::kCT] = make_float4(l[nb][0], l[nb][1], zs[nb][0], zs[nb][1]);
+            for (int nb = 0; nb < QB; ++nb) save[nb * S::kCT] = make_float2(l[nb][0], l[nb][1]);
             const uint32_t pst = pstore + half + koff * 2;
             const bool full = key0 + kWarpKeys - 1 <= min_lim && key0 > max_lo && (!TREE || key0 + kWarpKeys <= prior);
             // Once, and again with moved references where they do not stand (one
@@ -372,8 +368,8 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 ve = __reduce_max_sync(0xffffffffu, ve);
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
-                    const float4 v = save[nb * S::kCT];
-                    l[nb][0] = v.x, l[nb][1] = v.y, zs[nb][0] = v.z, zs[nb][1] = v.w;
+                    const float2 v = save[nb * S::kCT];
+                    l[nb][0] = v.x, l[nb][1] = v.y;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -407,6 +403,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                         l[nb][c] *= f[c];
                         f[c] *= fv;
                         zs[nb][c] *= f[c];
+                        zs[nb][2 + c] *= f[c];
                     }
 #pragma unroll
                     for (int mb = 0; mb < 4; ++mb) {
@@ -428,6 +425,14 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                     ptx::ldmatrix_x4(pload + half + nb * 8 * S::kPRow + kp * 64, pb[nb][0], pb[nb][1], pb[nb][2], pb[nb][3]);
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
+                    if (dh == 0) {  // the zero points' sum (16 equal rows)
+                        const uint32_t zw = sS + (kKT + kh * 64 + kp * 32 + kb * 16) * 4;
+                        const uint32_t z0 = zero_pair(lds32(zw + va * 4), lds32(zw + vb * 4));
+                        const uint32_t z8 = zero_pair(lds32(zw + va * 4 + 32), lds32(zw + vb * 4 + 32));
+                        const uint32_t a[4] = {z0, z0, z8, z8};
+#pragma unroll
+                        for (int nb = 0; nb < QB; ++nb) ptx::mma_f16_16816(zs[nb], a, pb[nb][2 * kb], pb[nb][2 * kb + 1]);
+                    }
                     const uint32_t pa = sV + vpiece_a + (kp * 32 + kb * 16) * S::kRowB, pc = sV + vpiece_b + (kp * 32 + kb * 16) * S::kRowB;
                     const uint32_t a0 = lds32(pa), b0 = lds32(pc), a8 = lds32(pa + 8 * S::kRowB), b8 = lds32(pc + 8 * S::kRowB);
 #pragma unroll
@@ -463,7 +468,6 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], d);
-                    zs[nb][c] += __shfl_xor_sync(0xffffffffu, zs[nb][c], d);
                 }
                 const int lr = nb * 8 + 2 * quad + c;
                 float e[8];  // dims 0 .. 7: blocks 0 .. 3 hold (0, 2), (4, 6), (1, 3), (5, 7)
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 d4[0] = make_float4(e[0], e[1], e[2], e[3]);
                 d4[1] = make_float4(e[4], e[5], e[6], e[7]);
                 if (g == 0) {
-                    lzbuf[warp * S::kRows + lr] = make_float2(l[nb][c], zs[nb][c] * real);
+                    lzbuf[warp * S::kRows + lr] = make_float2(l[nb][c], zs[nb][c] * 16777216.f * real);  // (0 with dh = 1)
                     if (gw == 0) mbuf[grp * S::kRows + lr] = (seen >> (2 * nb + c)) & 1u ? -nm[nb][c] : -INFINITY;
                 }
             }

@@ -158,7 +158,7 @@ struct RawRow {
         } else if (is_nan(other)) {
             s = 0x7FC07FC0u;
         }
-        const uint32_t z = 0x43004300u + (own & 0xFFu) * 0x00010001u;  // 128 + z, twice
+        const uint32_t z = 0x43004300u + (own & 15u) * 0x00010001u;  // 128 + z, twice
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int piece = (i + (r >> 1)) % kPieces;

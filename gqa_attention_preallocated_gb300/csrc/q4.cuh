@@ -3,8 +3,8 @@
 //
 // A row is one token of one KV head, K and V apart: d codes of 4 bits, eight
 // to a 32-bit word (value 2i at bits 4i, value 2i + 1 at bits 16 + 4i), and
-// one scale word (bf16 step s in the high 16 bits, zero point z in the low
-// 16).  A value is s * (c - z).
+// one scale word (bf16 step s in the high 16 bits, zero point z, 0 .. 15, in the
+// low 16, of which the lowest 4 count).  A value is s * (c - z).
 //
 // Why this order in a word: w & 0x000F000F, (w >> 4) & 0x000F000F, ... are then
 // pairs of neighbouring values, one per 16-bit half, which is how the packed
@@ -25,7 +25,7 @@ namespace q4 {
 constexpr float kMinStep = 1.17549435e-38f;  // 2^-126: a smaller step stores the row as zeros
 
 __device__ __forceinline__ float step_of(uint32_t scale_word) { return __uint_as_float(scale_word & 0xFFFF0000u); }
-__device__ __forceinline__ int zero_of(uint32_t scale_word) { return static_cast<int>(scale_word & 0xFFFFu); }
+__device__ __forceinline__ int zero_of(uint32_t scale_word) { return static_cast<int>(scale_word & 15u); }
 
 // Code of value e (0 .. 7) of a word.
 __device__ __forceinline__ int code_of(uint32_t w, int e) { return (w >> (((e & 1) << 4) + ((e >> 1) << 2))) & 15; }

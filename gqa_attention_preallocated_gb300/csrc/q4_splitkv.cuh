@@ -60,13 +60,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-__device__ __forceinline__ float2 f16x2_to_f32(uint32_t v) {
-    __half2 h;
-    memcpy(&h, &v, 4);
-    return __half22float2(h);
+// A scale word's zero point as a float.
+__device__ __forceinline__ float zero_f32(uint32_t scale_word) {
+    return __uint_as_float(0x4B000000u | (scale_word & 15u)) - 8388608.0f;
 }
-// A small unsigned integer (below 2^16) as a float.
-__device__ __forceinline__ float small_to_f32(uint32_t z) { return __uint_as_float(0x4B000000u | z) - 8388608.0f; }
+// Two keys' zero points as an f16 pair, z 2^-24 like the codes (an f16 subnormal).
+__device__ __forceinline__ uint32_t zero_pair(uint32_t word_a, uint32_t word_b) {
+    return ptx::prmt(word_a, word_b, 0x5410u) & 0x000F000Fu;
+}
 
 // What a row block's queries see: one past the last visible key, and the
 // smallest last key of a valid query (no key, and a large one, without any).

@@ -172,8 +172,8 @@ kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads
  * bits 4i and value 2i + 1 at bits 16 + 4i.  k_scales[l] / v_scales[l]:
  * 32-bit words [B, Hkv, S], S = max_len rounded up to a multiple of 4; word
  * [b][h][a] has s (bfloat16) in its high 16 bits and z in its low 16.  Other
- * producers may fill them (kvc_set_lens); codes need no check, a z above 15
- * counts as it stands.  head_dim is a multiple of 32, at most 256; all buffers
+ * producers may fill them (kvc_set_lens); of z the lowest 4 bits count.
+ * head_dim is a multiple of 32, at most 256; all buffers
  * are 16-byte aligned.  q, k_new, v_new and out are bf16.
  *
  * Every call of this header serves such a cache as it serves an FP8 one, with
