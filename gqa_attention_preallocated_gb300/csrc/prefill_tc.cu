@@ -27,17 +27,22 @@
 //
 // 4-bit caches (KVC_Q4; also d = 64): a tile's codes and scale words arrive by
 // untiled copies in raw slots, two for K and one for V, and four warps, a row a
-// thread, convert K, then V, into the bf16 tiles the MMAs read (all four on one
+// thread, convert K, then V, into the f16 tiles the MMAs read (all four on one
 // tensor: two warps for each of K and V took 236 us where this takes 207, B = 64,
 // S = 4096, 64 rows, as a tile's conversion stands in the way of its products).
-// A value is s * (c - z), rounded once to bf16: c - z is exact in bf16 and one product
-// rounds it, so the MMAs see what kvc_read gives.  (Folding the step into the
-// softmax instead, as the split-KV kernel does, would cost a multiply a score
-// and a weight, 256 rows x 128 keys a tile, where the conversion's is one a
-// value, 128 x 128, on warps that are otherwise idle; and f16 operands would
-// need a range check.)  A V row whose step is NaN is written as zeros and its K
-// row as NaN: the score carries the NaN to the queries that see the key, and
-// the others' zero weights meet a zero.
+// The operands are f16, whose 11 bits keep s * (c - z) (at most 12) nearly whole
+// where bf16 would round it to 8: the error of a chunk's output against 64 bits
+// is 0.0018 so, 0.0034 with bf16 rows and weights, 0.0017 of it the output's own
+// rounding.  f16's range is met with powers of two: each tile's K and V by the
+// largest step among them (K's goes back into the tile's scores, V's into the
+// tile's weights, relative to a reference that moves with O when a tile's is
+// larger), each query row by its largest value.  c - z is exact in f16 and one
+// product rounds it.  (Folding the step into the softmax instead, as the
+// split-KV kernel does, would cost a multiply a score and a weight, 256 rows x
+// 128 keys a tile, where the conversion's is one a value, 128 x 128, on warps
+// that are otherwise idle.)  A V row whose step is NaN is written as zeros and
+// its K row as NaN: the score carries the NaN to the queries that see the key,
+// and the others' zero weights meet a zero.
 //
 // Warp roles (12 warps, 14 for 4-bit caches):
 //   warp 0      TMA producer: Q tiles once, then K and V tiles (128 keys) into
@@ -115,7 +120,10 @@ constexpr int kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpt
 constexpr int kBarRawFull = 20, kBarRawEmpty = 23, kNumBars = 26;  // 4-bit caches' raw slots
 constexpr int kConvThreads = 64;  // warps 2 and 3
 constexpr size_t kSmemPF = 1024 + kOffBar + 256;
-constexpr size_t kSmemQ4 = kSmemPF + kRawSlots * kRawBytes;
+// ... then the query rows' score factors [2][128], and four tiles' step exponents
+// (K, V): tile j + 4's are written only after tile j's softmax.
+constexpr int kOffQFac = kOffRaw + kRawSlots * kRawBytes, kOffExp = kOffQFac + 2 * 128 * 4, kExpRing = 4;
+constexpr size_t kSmemQ4 = 1024 + kOffExp + kExpRing * 8 + 8;
 static_assert(kNumBars * 8 + 24 <= 256 && kSmemQ4 <= 232448, "shared memory map");
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -131,7 +139,7 @@ __device__ __forceinline__ uint32_t instr_desc(bool b_mn_major, bool f16, int n)
     return (1u << 4) | ab | (static_cast<uint32_t>(b_mn_major) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// 4-bit caches: row r of a raw slot (d / 2 bytes a row) into the bf16 tile the
+// 4-bit caches: row r of a raw slot (d / 2 bytes a row) into the f16 tile the
 // MMAs read (64-column boxes, 128-byte swizzle).  A thread owns a row and takes
 // its 16-byte pieces in an order that starts at r / 2, so that eight
 // neighbouring rows read eight different bank groups (their strides are 64
@@ -150,15 +158,17 @@ struct RawRow {
         own = is_v ? v : k;
         other = is_v ? k : v;
     }
-    __device__ __forceinline__ void convert(uint8_t* tile, int r, bool is_v) const {
+    // ex: exponent field of the tile's largest step; values are s (c - z) 2^(137 - ex).
+    __device__ __forceinline__ void convert(uint8_t* tile, int r, bool is_v, int ex) const {
         auto is_nan = [](uint32_t word) { return (word & 0x7FFF0000u) >= 0x7F800000u; };
-        uint32_t s = __byte_perm(own, 0, 0x3232);  // the step in both halves
+        const float step = q4::step_of(own) * __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
+        uint32_t s = ptx::pack_f16x2(step, step);
         if (is_v) {
             if (is_nan(own)) s = 0u;
         } else if (is_nan(other)) {
-            s = 0x7FC07FC0u;
+            s = 0x7E007E00u;
         }
-        const uint32_t z = 0x43004300u + (own & 15u) * 0x00010001u;  // 128 + z, twice
+        const uint32_t z = 0x64006400u + (own & 15u) * 0x00010001u;  // 1024 + z, twice
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int piece = (i + (r >> 1)) % kPieces;
@@ -168,8 +178,8 @@ struct RawRow {
                 uint32_t o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t c = ((u[k] >> (4 * e)) & 0x000F000Fu) | 0x43004300u;  // 128 + c, twice
-                    o[e] = ptx::mul_bf16x2(ptx::sub_bf16x2(c, z), s);
+                    const uint32_t c = ((u[k] >> (4 * e)) & 0x000F000Fu) | 0x64006400u;  // 1024 + c, twice
+                    o[e] = ptx::mul_f16x2(ptx::sub_f16x2(c, z), s);
                 }
                 const int cc = piece * 4 + k;  // 16-byte chunk of the row
                 *reinterpret_cast<uint4*>(tile + (cc >> 3) * kBoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4)) =
@@ -178,6 +188,33 @@ struct RawRow {
         }
     }
 };
+
+// 4-bit caches: query row r of a tile from bf16 to f16 in place, scaled by a power
+// of two to just below 2^15; returns the factor that takes it back.
+template <int kDim>
+__device__ __forceinline__ float convert_query_row(uint8_t* tile, int r) {
+    constexpr int kChunks = kDim / 8;
+    auto chunk = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int c = 0; c < kChunks; ++c) {
+        const uint4 v = *chunk(c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    }
+    const int e = max(16, static_cast<int>(top >> 7));
+    const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
+#pragma unroll 4
+    for (int c = 0; c < kChunks; ++c) {
+        const uint4 v = *chunk(c);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = ptx::pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
+        *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);  // 2^(e - 141)
+}
 
 // FP8 caches: one 128-key tile of E4M3 codes (128 rows x 128 bytes, 128-byte
 // swizzle) sits in the second half of a stage; convert it in place to the f16
@@ -367,10 +404,11 @@ __device__ __forceinline__ Piece decode_piece(const PrefillParams& p, int idx) {
 // piece's block in with cp.async, all of it in flight at once.  tS: this
 // head's S columns, idle by now, hold the running sum of O when a block has
 // more than two pieces.
-template <int kD>
+// kScaled: the own O takes o_scale to real units (4-bit caches).
+template <int kD, bool kScaled>
 __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t tS, uint32_t tO, int i, int r, bool valid,
                                             float m_ref, float l, int slot, int kidx, int npc, __nv_bfloat16* dst,
-                                            volatile int* merge_flag, float out_scale, float* stage, bool defer) {
+                                            volatile int* merge_flag, float out_scale, float* stage, bool defer, float o_scale) {
     constexpr int kRowF = kD + 4;             // floats per partial row: O, m, l, pad
     constexpr int kChunks = 128 * kRowF / 4;  // 16-byte chunks of one head's block
     static_assert(kChunks % 128 == 0, "each thread moves the same number of chunks");
@@ -385,6 +423,10 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
         uint32_t w[32];
         tmem_ld32(tO + c * 32, w);
         tmem_ld_wait();
+        if (kScaled) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * o_scale);
+        }
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<uint4*>(srow + c * 32 + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
@@ -456,7 +498,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
     if (npc == 2) {
         // o = w_1 O_1 + w_0 O_0 in one pass: the own O from TMEM, the other from
         // its staged block.
-        const float w_own = weight(kidx), w_oth = weight(1 - kidx);
+        const float w_own = weight(kidx) * (kScaled ? o_scale : 1.f), w_oth = weight(1 - kidx);
 #pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {
             uint32_t w[32];
@@ -482,7 +524,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
         for (int k = 0; k < npc; ++k) {
             const bool own = k == kidx, first = k == 0, last = k == npc - 1;
             if (!own) stage_piece(k);
-            const float wk = weight(k);
+            const float wk = weight(k) * (kScaled && own ? o_scale : 1.f);
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
                 float ok[32], acc[32];
@@ -527,7 +569,7 @@ __device__ __noinline__ void split_epilogue(float* partials, int* err, uint32_t 
 // alternate key tiles per TMEM buffer); modes 0 and 1 otherwise.  kF8: the
 // cache holds E4M3 codes (converted to f16 in shared memory by warps 2 and 3;
 // the MMAs run on f16 with the queries converted too; 4-bit rows are converted
-// to bf16 by four warps.  kD: the head dimension (64 with 4-bit storage only).
+// to f16 by four warps.  kD: the head dimension (64 with 4-bit storage only).
 template <bool kWin, bool kAlt, int kFmt, int kD>
 __global__ void __launch_bounds__(threads_pf(kFmt), 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap tmQ,
@@ -547,7 +589,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
 
     if (tid == 0) {
         const int ready = kQ4 ? 4 : kF8 ? 2 : 1;  // every converter warp arrives; else the TMA's arrive
-        ptx::mbar_init(bar(kBarQ), kF8 ? 2 : 1);
+        ptx::mbar_init(bar(kBarQ), ready);
         for (int s = 0; s < kRawSlots && kQ4; ++s) {
             ptx::mbar_init(bar(kBarRawFull + s), 1);
             ptx::mbar_init(bar(kBarRawEmpty + s), 4);
@@ -621,7 +663,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
-            const int qbar = kF8 ? kBarQRaw : kBarQ;
+            const int qbar = kF8 || kQ4 ? kBarQRaw : kBarQ;
             ptx::mbar_arrive_expect_tx(bar(qbar), nh * kBoxes * kBoxBytes);
             for (int i = 0; i < nh; ++i) {
                 // mode 0: 128 positions of head h0 + i; modes 1, 2: 128 packed rows
@@ -723,7 +765,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             ready(kBarVFull + s);
         }
     } else if (kQ4 && (warp == 2 || warp == 3 || warp >= 12)) {
-        // ------------------------------------------------------------ 4-bit -> bf16 converters
+        // ------------------------------------------------------------ 4-bit -> f16 converters
         const int r = warp >= 12 ? tid - 320 : tid - 64;  // this thread's row of a tile
         auto wait_for = [&](int b_idx, int parity) {
             if (!ptx::mbar_wait_bounded(bar(b_idx), parity, *abort_flag ? 0ull : kWaitNs)) {
@@ -731,26 +773,57 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 *abort_flag = 1;
             }
         };
+        auto arrive = [&](int b_idx) {  // generic writes -> visible to the tensor core, then arrive
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bar(b_idx));
+        };
+        volatile int2* exponents = reinterpret_cast<volatile int2*>(smem + kOffExp);
+        int ek = 0, ev = 0;  // exponent fields of the tile's largest steps
         auto convert = [&](int j, bool is_v) {
             // (K and V have slots of their own, and each slot's uses come to these
             // warps in order: an mbarrier's parity cannot tell phases two apart.)
             const int s = j & 1, sl = is_v ? 2 : s, turn = is_v ? j : j >> 1;
             RawRow<kD> row;
             wait_for(kBarRawFull + sl, turn & 1);
-            row.load(smem + kOffRaw + sl * kRawBytes, r, is_v);
+            const uint8_t* raw = smem + kOffRaw + sl * kRawBytes;
+            row.load(raw, r, is_v);
+            if (!is_v) {
+                // (K's slot holds both tensors' words; those past the last visible
+                // key, and NaN steps, do not count.  Every warp finds the same.)
+                const uint4 kw = *reinterpret_cast<const uint4*>(raw + kRawScaleK + lane * 16);
+                const uint4 vw = *reinterpret_cast<const uint4*>(raw + kRawScaleV + lane * 16);
+                const int live = kmax - (kt0 + j) * 128 - lane * 4;  // words 0 .. live of the four
+                const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w}, v4[4] = {vw.x, vw.y, vw.z, vw.w};
+                uint32_t a = 20, b2 = 20;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t x = (k4[i] >> 23) & 255u, y = (v4[i] >> 23) & 255u;
+                    if (i <= live && x != 255u) a = max(a, x);
+                    if (i <= live && y != 255u) b2 = max(b2, y);
+                }
+                ek = static_cast<int>(__reduce_max_sync(0xffffffffu, a));
+                ev = static_cast<int>(__reduce_max_sync(0xffffffffu, b2));
+                if (r == 0) {
+                    exponents[j % kExpRing].x = ek;
+                    exponents[j % kExpRing].y = ev;
+                }
+            }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));
             if (j >= 2) wait_for((is_v ? kBarVEmpty : kBarKEmpty) + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
-            row.convert(smem + (is_v ? kOffV : kOffK) + s * kTile128, r, is_v);
-            ptx::fence_proxy_async_smem();  // generic writes -> visible to the tensor core
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + s));
+            row.convert(smem + (is_v ? kOffV : kOffK) + s * kTile128, r, is_v, is_v ? ev : ek);
+            arrive((is_v ? kBarVFull : kBarKFull) + s);
         };
+        wait_for(kBarQRaw, 0);
+        for (int i = 0; i < nh; ++i)
+            reinterpret_cast<float*>(smem + kOffQFac)[i * 128 + r] = p.scale_log2 * convert_query_row<kD>(smem + kOffQ + i * kTile128, r);
+        arrive(kBarQ);
 #pragma unroll 1
         for (int n = 0; n < 2 * nkt; ++n) convert(n >> 1, (n & 1) != 0);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t id_qk = instr_desc(false, kF8, 128), id_pv = instr_desc(true, kF8, kD);
+        const uint32_t id_qk = instr_desc(false, kF8 || kQ4, 128), id_pv = instr_desc(true, kF8 || kQ4, kD);
         auto wait = [&](int b_idx, int parity) {
             if (!ptx::mbar_wait_bounded(bar(b_idx), parity, *abort_flag ? 0ull : kWaitNs)) {
                 atomicExch(p.err, kDevTimeoutFull);
@@ -871,7 +944,13 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             const int nloc = alt ? (nkt - i + 1) / 2 : nkt;
             const int lo_row = (kWin && valid) ? lim - p.window : -(1 << 30);  // keys <= lo_row: outside the window
             // score scale in base 2 (times the K scale of an FP8 cache)
-            const float sl2 = kF8 ? p.scale_log2 * p.kscale[kvh] : p.scale_log2;
+            float sl2 = kF8 ? p.scale_log2 * p.kscale[kvh] : p.scale_log2;
+            // 4-bit: the query row's factor, read behind its first scores; exponent
+            // that V's steps, and so O, are relative to (two above the first
+            // tile's, so that it seldom moves)
+            float q_factor = 0.f;
+            int v_ref = 0;
+            volatile int2* exponents = reinterpret_cast<volatile int2*>(smem + kOffExp);
             float m_ref = -INFINITY, l = 0.f;
             for (int jj = 0; jj < nloc; ++jj) {
                 const int j = jfirst + jj * jstep;
@@ -880,6 +959,14 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                     *abort_flag = 1;
                 }
                 tc_fence_after();
+                int v_exp = 0;  // the tile's V exponent less the reference
+                if constexpr (kQ4) {
+                    if (jj == 0) q_factor = reinterpret_cast<volatile float*>(smem + kOffQFac)[(alt ? 0 : i) * 128 + r];
+                    const int ek = exponents[j % kExpRing].x, ev = exponents[j % kExpRing].y;
+                    sl2 = q_factor * __uint_as_float(static_cast<uint32_t>(max(1, ek - 10)) << 23);  // 2^(ek - 137)
+                    if (jj == 0) v_ref = ev + 2;
+                    v_exp = max(ev - v_ref, -40);  // (below that a weight leaves nothing in f16, and its sum is kept)
+                }
                 const bool full_tile = ((kt0 + j) * 128 + 127 <= full_below) && (!kWin || (kt0 + j) * 128 > max_lo);
                 const int key0 = (kt0 + j) * 128;
                 // pass 1: row max of the raw scores (scale > 0, so it scales after);
@@ -907,13 +994,19 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 }
                 mx = (mx == -INFINITY) ? -INFINITY : mx * sl2;
                 const bool move = mx > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mx != -INFINITY);
-                if (__any_sync(0xffffffffu, move)) {
+                if (__any_sync(0xffffffffu, move || (kQ4 && v_exp > 0))) {
                     // Move the reference max.  O_i holds the PV sums up to tile
                     // j-1 (all with the old reference): wait for the last of them
                     // and scale O_i and l by 2^(old - new).  The TMEM loads and
                     // stores are warp-collective, so the warp rescales together;
                     // rows that keep their reference scale by 1.
                     const float f = !move ? 1.f : (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - mx);
+                    float fo = f;  // O's factor: V's exponent moves too
+                    if (kQ4 && v_exp > 0) {
+                        fo *= v_exp + 2 < 127 ? __uint_as_float(static_cast<uint32_t>(125 - v_exp) << 23) : 0.f;
+                        v_ref += v_exp + 2;
+                        v_exp = -2;
+                    }
                     if (jj > 0) {
                         if (!ptx::mbar_wait_bounded(bar(kBarO + i), (jj - 1) & 1, *abort_flag ? 0ull : kWaitNs)) {
                             atomicExch(p.err, kDevTimeoutFull);
@@ -928,7 +1021,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(v[h * 32 + e]) * f);
+                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(v[h * 32 + e]) * fo);
                                 tmem_st32(tO + c * 64 + h * 32, w);
                             }
                         }
@@ -939,7 +1032,8 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 }
                 // pass 2: p = 2^(s * scale - m_ref) as bf16 pairs into TMEM over S_i
                 const float mu = (m_ref == -INFINITY) ? 0.f : m_ref;
-                const uint64_t sc2 = f2pack(sl2, sl2), nmu2 = f2pack(-mu, -mu);
+                const float add = kQ4 ? static_cast<float>(v_exp) - mu : -mu;
+                const uint64_t sc2 = f2pack(sl2, sl2), nmu2 = f2pack(add, add);
                 uint64_t sum2 = f2pack(0.f, 0.f);
                 uint32_t pk[32];
 #pragma unroll 1
@@ -958,7 +1052,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                             if (e + 1 > kl || e + 1 <= kll) p1 = 0.f;
                         }
                         sum2 = fadd2(sum2, f2pack(p0, p1));
-                        pk[e >> 1] = kF8 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+                        pk[e >> 1] = kF8 || kQ4 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
                     }
                     // keys c*64 .. c*64+63 -> P columns c*32 .. c*32+31 (S columns already read)
                     tmem_st32(tS + c * 32, pk);
@@ -966,7 +1060,9 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 {
                     float s0, s1;
                     f2unpack(sum2, s0, s1);
-                    l += s0 + s1;
+                    // (the weights' power of two does not belong to their sum)
+                    if (kQ4) l = fmaf(s0 + s1, __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23), l);
+                    else l += s0 + s1;
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -986,6 +1082,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 // O_1 directly once warpgroup 1 has seen its last PV land.
                 float* ml1 = reinterpret_cast<float*>(smem + kOffQ + kTile128);  // second Q tile: unused here
                 if (i == 1) {
+                    if (kQ4 && r == 0) ml1[256] = static_cast<float>(v_ref);
                     ml1[r] = m_ref;
                     ml1[128 + r] = l;
                 }
@@ -998,6 +1095,8 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                     const float Mu = (M == -INFINITY) ? 0.f : M;
                     const float f0 = (m_ref == -INFINITY) ? 0.f : ptx::ex2(m_ref - Mu);
                     const float f1 = (m1 == -INFINITY) ? 0.f : ptx::ex2(m1 - Mu);
+                    // (4-bit: O_1 in O_0's units)
+                    const float fo1 = kQ4 ? f1 * ptx::ex2(ml1[256] - static_cast<float>(v_ref)) : f1;
 #pragma unroll 1
                     for (int c = 0; c < kD / 32; ++c) {
                         uint32_t w0[32], w1[32];
@@ -1006,7 +1105,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                         tmem_ld_wait();
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            w0[e] = __float_as_uint(__uint_as_float(w0[e]) * f0 + __uint_as_float(w1[e]) * f1);
+                            w0[e] = __float_as_uint(__uint_as_float(w0[e]) * f0 + __uint_as_float(w1[e]) * fo1);
                         tmem_st32(tO + c * 32, w0);
                     }
                     tmem_st_wait();
@@ -1018,15 +1117,16 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             const int qrow = (p.mode == 0) ? ((b * p.Hq) + h0 + i) * p.T + t0 + r
                                            : (b * p.Hq + h0) * p.T + pc.pr0 + (alt ? 0 : i * 128) + r;
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(qrow) * kD;
+            const float o_scale = kQ4 ? __uint_as_float(static_cast<uint32_t>(v_ref - 10) << 23) : 1.f;  // 2^(v_ref - 137)
             if (alt && i == 1) {
                 // state handed to warpgroup 0
             } else if (pc.slot != kPrefillNoSlot) {
-                split_epilogue<kD>(p.partials, p.err, tS, tO, i, r, valid, m_ref, l, pc.slot, pc.kidx, pc.npc, dst, merge_flag,
+                split_epilogue<kD, kQ4>(p.partials, p.err, tS, tO, i, r, valid, m_ref, l, pc.slot, pc.kidx, pc.npc, dst, merge_flag,
                                kF8 ? p.vscale[kvh] : 1.f,
                                reinterpret_cast<float*>(smem + kOffQ + i * kSplitStageBytes),
-                               p.defer_pieces > 0 && pc.npc >= p.defer_pieces);
+                               p.defer_pieces > 0 && pc.npc >= p.defer_pieces, o_scale);
             } else {
-            const float inv = (valid && l > 0.f) ? (kF8 ? p.vscale[kvh] : 1.f) / l : 0.f;
+            const float inv = (valid && l > 0.f) ? (kF8 ? p.vscale[kvh] : o_scale) / l : 0.f;
 #pragma unroll
             for (int c = 0; c < kD / 32; ++c) {
                 uint32_t w[32];

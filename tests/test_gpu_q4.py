@@ -79,13 +79,13 @@ def _bound(want, mass, dot, add, rows):
     """Largest |got - want| that the kernels' roundings allow.
 
     The output is rounded to bf16.  Up to 32 query rows per KV head (and in
-    trees) the codes and queries enter the products exactly and only the softmax weights are
-    rounded, to f16.  Above, the rows are rounded to bf16 on their way to the
-    tensor core (K: each score moves by at most UB * sum |q k| / sqrt d, so each
-    weight by twice that; V: by UB) and the weights too.  float32 sums, exp2
-    and the norm add 2^-16 of the mass, and 2^-20 * sum |q k| / sqrt d in the
-    scores."""
-    up, uv, uk = (U16, 0.0, 0.0) if rows <= 32 else (UB, UB, UB)
+    trees) the codes and queries enter the products exactly and only the softmax
+    weights are rounded, to f16.  Above, the rows are rounded to f16 on their way
+    to the tensor core (K: each score moves by at most U16 * sum |q k| / sqrt d,
+    so each weight by twice that; V: by U16) and the weights too.  float32 sums,
+    exp2 and the norm add 2^-16 of the mass, and 2^-20 * sum |q k| / sqrt d in
+    the scores."""
+    up, uv, uk = (U16, 0.0, 0.0) if rows <= 32 else (U16, U16, U16)
     shift = 2 * np.expm1((uk + 2.0 ** -20) * dot)
     return UB * np.abs(want) + mass * (1 + UB) * (up + uv + shift + 2.0 ** -16) + add + 1e-30
 
@@ -366,6 +366,25 @@ def test_scales_of_very_different_size():
         q = _bf(q.double() * scale)
         out = p.c.gqa_attention(0, q.cuda(), [T, T])
         p.check_out(out, q, [T, T], T, tag=(T, scale))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T", [(4, 100), (2, 150), (8, 10)])
+def test_steps_that_change_from_tile_to_tile(d, G, T):
+    """V of some tiles is all zeros, of others 2^12 times the last tile's; K's too: the tiles' powers of two move."""
+    p = Pair(2, 1, d, 1100, seed=d + T)
+    n = 900
+    q, k, v = p.inputs([n, n], n, 1)
+    at = torch.arange(n)[None, None, :, None]
+    v = _bf(torch.where(at < 256, torch.zeros(()), v.double() * 2.0 ** (4.0 * (at // 128)).double() * (at // 128 % 3 != 0)))
+    k = _bf(k.double() * torch.where(at // 128 % 2 == 0, 2.0 ** -6, 1.0).double())
+    p.c.append(0, k.cuda(), v.cuda(), [n, n])
+    p.note(k, v, [n, n])
+    p.step([T, T - 3], G, T=T)
+    p.c.truncate([120, 240])  # nothing but zeros before the chunk
+    for x in p.x:
+        x[0], x[1] = x[0][:, :120], x[1][:, :240]
+    p.step([T, 1], G, T=T)
 
 
 def test_nan_rows_reach_their_queries_only():
