@@ -195,20 +195,21 @@ template <int kDim>
 __device__ __forceinline__ float convert_query_row(uint8_t* tile, int r) {
     constexpr int kChunks = kDim / 8;
     auto chunk = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
+    uint4 v[kChunks];
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) v[c] = *chunk(c);
+#pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const uint4 v = *chunk(c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
     }
     const int e = max(16, static_cast<int>(top >> 7));
     const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
-#pragma unroll 4
+#pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-        const uint4 v = *chunk(c);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = ptx::pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
         *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -787,28 +788,32 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             RawRow<kD> row;
             wait_for(kBarRawFull + sl, turn & 1);
             const uint8_t* raw = smem + kOffRaw + sl * kRawBytes;
-            row.load(raw, r, is_v);
             if (!is_v) {
-                // (K's slot holds both tensors' words; those past the last visible
-                // key, and NaN steps, do not count.  Every warp finds the same.)
-                const uint4 kw = *reinterpret_cast<const uint4*>(raw + kRawScaleK + lane * 16);
-                const uint4 vw = *reinterpret_cast<const uint4*>(raw + kRawScaleV + lane * 16);
+                // The tile's largest steps (K's slot holds both tensors' words), the
+                // same in every warp.  Scale words order like integers; adding one
+                // to the exponent makes NaN and infinite steps negative, so that
+                // they do not count, nor do words past the last visible key.
+                int4 kw = *reinterpret_cast<const int4*>(raw + kRawScaleK + lane * 16);
+                int4 vw = *reinterpret_cast<const int4*>(raw + kRawScaleV + lane * 16);
                 const int live = kmax - (kt0 + j) * 128 - lane * 4;  // words 0 .. live of the four
-                const uint32_t k4[4] = {kw.x, kw.y, kw.z, kw.w}, v4[4] = {vw.x, vw.y, vw.z, vw.w};
-                uint32_t a = 20, b2 = 20;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t x = (k4[i] >> 23) & 255u, y = (v4[i] >> 23) & 255u;
-                    if (i <= live && x != 255u) a = max(a, x);
-                    if (i <= live && y != 255u) b2 = max(b2, y);
+                if (kt0 + j == nkt_all - 1) {
+                    if (live < 0) kw.x = vw.x = 0;
+                    if (live < 1) kw.y = vw.y = 0;
+                    if (live < 2) kw.z = vw.z = 0;
+                    if (live < 3) kw.w = vw.w = 0;
                 }
-                ek = static_cast<int>(__reduce_max_sync(0xffffffffu, a));
-                ev = static_cast<int>(__reduce_max_sync(0xffffffffu, b2));
+                constexpr uint32_t kOne = 1u << 23;
+                auto up = [](int w) { return static_cast<int>(static_cast<uint32_t>(w) + kOne); };
+                const int a = max(max(up(kw.x), up(kw.y)), max(up(kw.z), up(kw.w)));
+                const int b2 = max(max(up(vw.x), up(vw.y)), max(up(vw.z), up(vw.w)));
+                ek = max(20, (__reduce_max_sync(0xffffffffu, a) >> 23) - 1);
+                ev = max(20, (__reduce_max_sync(0xffffffffu, b2) >> 23) - 1);
                 if (r == 0) {
                     exponents[j % kExpRing].x = ek;
                     exponents[j % kExpRing].y = ev;
                 }
             }
+            row.load(raw, r, is_v);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));
             if (j >= 2) wait_for((is_v ? kBarVEmpty : kBarKEmpty) + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
