@@ -35,11 +35,16 @@ using namespace q4;
 template <int QB>
 struct WideShape {
     static constexpr int D = 128;
-    // Groups of four warps: as many as leave a thread the registers it needs.
-    static constexpr int kGroups = QB == 2 ? 3 : 2;
+    static constexpr int kGroups = 3;                 // of four warps
+    // Blocks of 16 keys scored side by side, as many as the registers hold.
+    static constexpr int kChunks = QB == 4 ? 1 : 2;
     static constexpr int kCW = kGroups * kTileWarps;
     static constexpr int kCT = kCW * 32;
-    static constexpr int kThreads = kCT + 32 * kGroups;
+    static constexpr int kThreads = kCT + 128;        // a warpgroup copies (a warp a group of the others)
+    // Registers of a computing and of a copying thread after the split:
+    // 384 x 160 + 128 x 32 = 512 x 128, what they have at launch.
+    static constexpr int kRegs = 160, kCopyRegs = 32;
+    static_assert(kCT * kRegs + 128 * kCopyRegs <= 65536 && kThreads * 128 == 65536, "register split");
     static constexpr int kRows = 8 * QB;
     static constexpr int kStageB = Stage<D>::kBytes, kRowB = Stage<D>::kRowB, kCodeB = Stage<D>::kCodeB;
     static constexpr int kPS = D + 4;                 // floats of a partial's row: O, m, l, pad
@@ -49,14 +54,15 @@ struct WideShape {
     // warp's maxima [group][warp][row] and exponents, sums l and the zero points'
     // [group][warp][row], references of a group [group][row], sums set aside
     // [block][thread].
-    static constexpr int kObuf = kGroups * 2 * kRows * kPS * 4;
+    static constexpr int kObuf = kGroups * kRows * kPS * 4;
     static constexpr int kPhalf = kRows * kPRow;      // one tile's weights of a group; two of them
     static constexpr int kPbuf = kGroups * 2 * kPhalf;
     static constexpr int kSave = QB * kCT * 8;        // l set aside, 8 bytes a thread and block
     static constexpr int kQbuf = QB * 4 * 32 * 16;
-    static constexpr int kOffP = kObuf, kOffQ = kOffP + kPbuf, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 8,
+    static constexpr int kTile = kPbuf + kSave;       // (used within a segment, states only at its end)
+    static constexpr int kOffP = 0, kOffSave = kPbuf, kOffQ = kObuf > kTile ? kObuf : kTile, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 8,
                          kOffVe = kOffMx + kCW * kRows * 4, kOffLz = kOffVe + 64, kOffM = kOffLz + kCW * kRows * 8,
-                         kOffSave = kOffM + kGroups * kRows * 4, kMisc = kOffSave + kSave;
+                         kMisc = kOffM + kGroups * kRows * 4;
     static constexpr int kFit = (232448 - 1024 - 512 - kMisc) / kStageB;
     static constexpr int kStages = kFit / kGroups * kGroups;
     static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kMisc + 2 * kStages * 8 + 16 + sizeof(Segment);
@@ -81,6 +87,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     decode_q4_wide_kernel(const __grid_constant__ DecodeParams p) {
     using S = WideShape<QB>;
     constexpr int D = S::D, kStages = S::kStages, PS = S::kPS;
+    constexpr int kChunks = S::kChunks;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -124,11 +131,14 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     if (x0 >= x1) return;
 
     if (warp >= S::kCW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kCopyRegs));
+        if (warp >= S::kCW + S::kGroups) return;
         produce<D, kStages, S::kGroups, DP>(p, wp, x0, x1, warp - S::kCW, lane, stage0, bar0, abort_flag);
         return;
     }
 
     // ------------------------------------------------------------------ consumers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
     const int grp = warp / kTileWarps, gw = warp % kTileWarps;
     const int kh = gw >> 1, dh = gw & 1;  // output: this warp's half of the keys and of the dims
     const int koff = gw * kWarpKeys;      // scores: its keys of a tile
@@ -242,36 +252,13 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
         }
         constexpr uint32_t kAll = (1u << (2 * QB)) - 1;
 
-        // The weights of 16 keys from key0 (row `at` of the tile) on, written at
-        // `pst`; the rows' maxima, relative to the references, into mx, V's largest
-        // exponent into ve.  full: every valid query of the block sees every key.
+        // From raw scores to weights, for 16 keys from key0 on: the weights written
+        // at `pst`, the rows' maxima, relative to the references, into mx, V's
+        // largest exponent into ve.  full: every valid query of the block sees every
+        // key.
         float mx[QB][2];
         uint32_t ve;
-        auto weigh = [&](const bool full, const int key0, const int at, const uint32_t sK, const uint32_t sS, const uint32_t pst) {
-            uint32_t kw[2], vw[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                kw[h] = lds32(sS + (at + kg + 8 * h) * 4);
-                vw[h] = lds32(sS + (kKT + at + kg + 8 * h) * 4);
-            }
-            const uint4 k0 = ptx::ld_shared_v4(sK + kpiece + at * S::kRowB), k1 = ptx::ld_shared_v4(sK + kpiece + (at + 8) * S::kRowB);
-            const uint32_t k0w[4] = {k0.x, k0.y, k0.z, k0.w}, k1w[4] = {k1.x, k1.y, k1.z, k1.w};
-            // S^T in base 2 less the references, masked.
-            float sc[QB][4];
-#pragma unroll
-            for (int nb = 0; nb < QB; ++nb) sc[nb][0] = sc[nb][1] = sc[nb][2] = sc[nb][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t x0w = k0w[i], x1w = k1w[i], y0w = x0w >> 8, y1w = x1w >> 8;
-                const uint32_t a[4] = {x0w & 0x000F000Fu, x1w & 0x000F000Fu, x0w & 0x00F000F0u, x1w & 0x00F000F0u};
-                const uint32_t c[4] = {y0w & 0x000F000Fu, y1w & 0x000F000Fu, y0w & 0x00F000F0u, y1w & 0x00F000F0u};
-#pragma unroll
-                for (int nb = 0; nb < QB; ++nb) {
-                    const uint4 f = ptx::ld_shared_v4(misc0 + S::kOffQ + ((nb * 4 + i) * 32 + lane) * 16);
-                    ptx::mma_f16_16816(sc[nb], a, f.x, f.y);
-                    ptx::mma_f16_16816(sc[nb], c, f.z, f.w);
-                }
-            }
+        auto settle = [&](const bool full, const int key0, uint32_t (&kw)[2], uint32_t (&vw)[2], float (&sc)[QB][4], const uint32_t pst) {
             if (!full) {
                 // (Keys that no query of the block sees: no step, so that neither a
                 // stale word nor its exponent enters.)
@@ -331,6 +318,45 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 16), "r"(transpose8x8(h1)) : "memory");
             }
         };
+        // The same for 16 kChunks keys from key0 (row `at` of the tile) on.
+        auto weigh = [&](const bool full, const int key0, const int at, const uint32_t sK, const uint32_t sS, const uint32_t pst) {
+            // S^T of all its keys first: 2 QB chains of products side by side, and a
+            // query fragment read once for them.
+            float sa[kChunks][QB][4];
+            uint32_t kwa[kChunks][2], vwa[kChunks][2], kc[kChunks][2][4];
+#pragma unroll
+            for (int u = 0; u < kChunks; ++u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    kwa[u][h] = lds32(sS + (at + 16 * u + kg + 8 * h) * 4);
+                    vwa[u][h] = lds32(sS + (kKT + at + 16 * u + kg + 8 * h) * 4);
+                    const uint4 c = ptx::ld_shared_v4(sK + kpiece + (at + 16 * u + 8 * h) * S::kRowB);
+                    kc[u][h][0] = c.x, kc[u][h][1] = c.y, kc[u][h][2] = c.z, kc[u][h][3] = c.w;
+                }
+#pragma unroll
+                for (int nb = 0; nb < QB; ++nb) sa[u][nb][0] = sa[u][nb][1] = sa[u][nb][2] = sa[u][nb][3] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a[kChunks][4], c[kChunks][4];
+#pragma unroll
+                for (int u = 0; u < kChunks; ++u) {
+                    const uint32_t x0w = kc[u][0][i], x1w = kc[u][1][i], y0w = x0w >> 8, y1w = x1w >> 8;
+                    a[u][0] = x0w & 0x000F000Fu, a[u][1] = x1w & 0x000F000Fu, a[u][2] = x0w & 0x00F000F0u, a[u][3] = x1w & 0x00F000F0u;
+                    c[u][0] = y0w & 0x000F000Fu, c[u][1] = y1w & 0x000F000Fu, c[u][2] = y0w & 0x00F000F0u, c[u][3] = y1w & 0x00F000F0u;
+                }
+#pragma unroll
+                for (int nb = 0; nb < QB; ++nb) {
+                    const uint4 f = ptx::ld_shared_v4(misc0 + S::kOffQ + ((nb * 4 + i) * 32 + lane) * 16);
+#pragma unroll
+                    for (int u = 0; u < kChunks; ++u) ptx::mma_f16_16816(sa[u][nb], a[u], f.x, f.y);
+#pragma unroll
+                    for (int u = 0; u < kChunks; ++u) ptx::mma_f16_16816(sa[u][nb], c[u], f.z, f.w);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kChunks; ++u) settle(full, key0 + 16 * u, kwa[u], vwa[u], sa[u], pst + u * 32);
+        };
 
         for (uint32_t half = 0; mine < it_end; mine += S::kGroups, half ^= S::kPhalf) {
             // (On expiry as in decode_q4.cu: record it and carry on.)
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) mx[nb][0] = mx[nb][1] = -INFINITY;
 #pragma unroll 1
-                for (int k = 0; k < kWarpKeys; k += 16) weigh(full, key0 + k, koff + k, sK, sS, pst + k * 2);
+                for (int k = 0; k < kWarpKeys; k += 16 * kChunks) weigh(full, key0 + k, koff + k, sK, sS, pst + k * 2);
                 bool move = seen != kAll || ve > vexp;
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) move |= fmaxf(mx[nb][0], mx[nb][1]) > kLazyRescale;
@@ -459,8 +485,12 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
             }
         }
 
-        // The segment's end: the groups' states into shared memory in real units.
+        // The segment's end: the groups' states into shared memory (over the weights,
+        // once no warp reads them) in real units.
+        ptx::named_barrier_sync(1, S::kCT);
         const float real = 0.015625f * __uint_as_float(vexp << 23);  // 2^(vexp - 133), as a product that stays normal
+        // (Keys' second halves are added to the first.)
+        if (kh == 1) ptx::named_barrier_sync(2 + grp, 128);
 #pragma unroll
         for (int nb = 0; nb < QB; ++nb)
 #pragma unroll
@@ -477,7 +507,12 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                     e[v] = o[nb][mb][c] * 16777216.f * real;
                     e[v + 2] = o[nb][mb][2 + c] * 1048576.f * real;
                 }
-                float4* d4 = reinterpret_cast<float4*>(obuf + ((grp * 2 + kh) * S::kRows + lr) * PS + dh * 64 + g * 8);
+                float4* d4 = reinterpret_cast<float4*>(obuf + (grp * S::kRows + lr) * PS + dh * 64 + g * 8);
+                if (kh == 1) {
+                    const float4 u = d4[0], v = d4[1];
+                    e[0] += u.x, e[1] += u.y, e[2] += u.z, e[3] += u.w;
+                    e[4] += v.x, e[5] += v.y, e[6] += v.z, e[7] += v.w;
+                }
                 d4[0] = make_float4(e[0], e[1], e[2], e[3]);
                 d4[1] = make_float4(e[4], e[5], e[6], e[7]);
                 if (g == 0) {
@@ -485,6 +520,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                     if (gw == 0) mbuf[grp * S::kRows + lr] = (seen >> (2 * nb + c)) & 1u ? -nm[nb][c] : -INFINITY;
                 }
             }
+        if (kh == 0) ptx::named_barrier_sync(2 + grp, 128);
         ptx::named_barrier_sync(1, S::kCT);
         // Merge the groups in their order, and write the unit's output (this CTA
         // saw all of it) or the CTA's partial.
@@ -516,13 +552,12 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < S::kGroups; ++i) {
                 const float f = ptx::ex2(gm[i] - Mu);
-                const float4 u = reinterpret_cast<const float4*>(obuf + ((i * 2) * S::kRows + lr) * PS)[c4];
-                const float4 v = reinterpret_cast<const float4*>(obuf + ((i * 2 + 1) * S::kRows + lr) * PS)[c4];
+                const float4 u = reinterpret_cast<const float4*>(obuf + (i * S::kRows + lr) * PS)[c4];
                 L = fmaf(gl[i], f, L);
-                acc.x = fmaf(u.x + v.x - gz[i], f, acc.x);
-                acc.y = fmaf(u.y + v.y - gz[i], f, acc.y);
-                acc.z = fmaf(u.z + v.z - gz[i], f, acc.z);
-                acc.w = fmaf(u.w + v.w - gz[i], f, acc.w);
+                acc.x = fmaf(u.x - gz[i], f, acc.x);
+                acc.y = fmaf(u.y - gz[i], f, acc.y);
+                acc.z = fmaf(u.z - gz[i], f, acc.z);
+                acc.w = fmaf(u.w - gz[i], f, acc.w);
             }
             write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + blockIdx.x, lr);
         }
