@@ -78,19 +78,19 @@ struct Q4Shape {
     static constexpr int kRowB = Stage<D>::kRowB, kCodeB = Stage<D>::kCodeB, kStageB = Stage<D>::kBytes;
     static constexpr int kPS = D + 4;              // floats of a state's row: O, m, l, pad
     static constexpr size_t kObuf = static_cast<size_t>(kCW) * kRows * kPS * sizeof(float);
-    static constexpr int kFit = static_cast<int>((232448 - 1024 - 512 - 4096 - kObuf) / kStageB);
+    static constexpr bool kQSmem = QB > 2;  // query fragments in shared memory, not in registers
+    static constexpr size_t kQgroup = kQSmem ? QB * (D / 32) * 32 * 16 : 0, kQbuf = kGroups * kQgroup;
+    static constexpr int kFit = static_cast<int>((232448 - 1024 - 512 - kQbuf - kObuf) / kStageB);
     // A multiple of the groups, so that a stage belongs to one of them and a
     // stage's phases reach its warps in order.
     static constexpr int kStages = (kFit < 20 ? kFit : 20) / kGroups * kGroups;
-    static constexpr bool kQSmem = QB > 2;  // query fragments in shared memory, not in registers
-    static constexpr size_t kQbuf = kQSmem ? QB * (D / 32) * 32 * 16 : 0;
-    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + kQbuf + 2 * kStages * 8 + 16 + sizeof(Segment);
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kObuf + kQbuf + 2 * kStages * 8 + 16 + kGroups * sizeof(Segment);
     static_assert(kStages >= 2 * kGroups, "a stage to read and one to fill for every group");
-    static_assert(kSmem <= 232448, "shared memory per CTA");
+    static_assert(kSmem <= 232448 && kGroups == q4_groups(D, kRows), "shared memory per CTA");
 };
 
 // DP: the partition comes from a device plan; TREE: draft-tree ancestor masks.
-template <int D, int QB, bool DP, bool TREE>
+template <int D, int QB, bool DP, bool TREE, bool SPLIT>
 __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     decode_q4_kernel(const __grid_constant__ DecodeParams p) {
     using S = Q4Shape<D, QB>;
@@ -110,14 +110,10 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     const uint32_t qfrag = ptx::smem_addr(qbuf);
     uint64_t* bars = reinterpret_cast<uint64_t*>(qbuf + S::kQbuf);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages);
-    volatile Segment* seg = reinterpret_cast<volatile Segment*>(bars + 2 * kStages + 2);
+    volatile Segment* segs = reinterpret_cast<volatile Segment*>(bars + 2 * kStages + 2);  // a group's
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Part<DP> wp{p};
-    long long N = DP ? 0 : wp.total_tiles();
-    long long P = gridDim.x;
-    int x0 = static_cast<int>(static_cast<long long>(blockIdx.x) * N / P);
-    int x1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * N / P);
 
     const uint32_t stage0 = ptx::smem_addr(smem);
     const uint32_t bar0 = ptx::smem_addr(bars);  // full[s] = bar0 + 8s, empty[s] = bar0 + 8(kStages + s)
@@ -132,27 +128,24 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     __syncthreads();
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    if (DP) {
-        if (p.dplan->skip) return;  // a rejected device-resident step: nothing is written
-        N = wp.total_tiles();
-        // (With the counters every CTA of a unit's range must have a tile: no more
-        // CTAs than tiles, as the host's plan has it.)
-        if (p.counters) P = min(P, max(N, 1ll));
-        const long long i = min(static_cast<long long>(blockIdx.x), P);
-        x0 = static_cast<int>(i * N / P);
-        x1 = static_cast<int>(min(i + 1, P) * N / P);
-    }
+    if (DP && p.dplan->skip) return;  // a rejected device-resident step: nothing is written
 
     zero_padded_queries<D, DP>(p, wp, tid, S::kThreads);
+    const int grp = warp < S::kCW ? warp / kTileWarps : warp - S::kCW;
+    const Party<S::kGroups, SPLIT> party{grp};
+    int x0, x1;  // this party's tiles
+    {
+        const long long N = wp.total_tiles(), P = shares(wp), i = party.part();
+        x0 = static_cast<int>(min(i, P) * N / P), x1 = static_cast<int>(min(i + 1, P) * N / P);
+    }
     if (x0 >= x1) return;
 
     if (warp >= S::kCW) {
-        produce<D, kStages, S::kGroups, DP>(p, wp, x0, x1, warp - S::kCW, lane, stage0, bar0, abort_flag);
+        produce<D, kStages, DP>(p, wp, x0, x1, party, lane, stage0, bar0, abort_flag);
         return;
     }
 
     // ------------------------------------------------------------------ consumers
-    const int grp = warp / kTileWarps;                 // this warp's tiles: those of its group
     const int koff = (warp % kTileWarps) * kWarpKeys;  // its keys of a tile
     const int quad = lane & 3, g = lane >> 2;
     const int kg = perm8<D>(g);                                    // K: key of accumulator row g (and + 8)
@@ -164,7 +157,8 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 
     Cursor<DP, kKT> cur;
     cur.init(wp, x0);
-    int mine = grp, stage = grp, phase = 0;  // this warp's next tile of the CTA's sequence, its stage and parity
+    volatile Segment* seg = segs + grp;
+    int mine = party.first_tile(), stage = grp, phase = 0;  // this warp's next tile of the CTA's sequence, its stage and parity
 
     for (int x = x0; x < x1;) {
         // One segment: this CTA's tiles of one unit.
@@ -187,7 +181,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             lane_lim = (lane < S::kRows && r < p.R && t < nn) ? prior + t : -1;
         }
         const uint32_t valid = __ballot_sync(0xffffffffu, lane_lim >= 0);
-        if (tid == 0) {
+        if ((tid & 127) == 0) {
             seg->row0 = row0;
             seg->valid = valid;
             seg->unit_tile = x - j0;
@@ -236,7 +230,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     }
                     qa[nb][i] = make_uint4(hq[0], hq[1], hq[2], hq[3]);
                     if constexpr (S::kQSmem) {
-                        if (warp == nb) *reinterpret_cast<uint4*>(qbuf + ((nb * KW + i) * 32 + lane) * 16) = qa[nb][i];
+                        if (warp % kTileWarps == nb) *reinterpret_cast<uint4*>(qbuf + grp * S::kQgroup + ((nb * KW + i) * 32 + lane) * 16) = qa[nb][i];
                     }
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -249,7 +243,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             }
         }
 
-        if constexpr (S::kQSmem) ptx::named_barrier_sync(1, S::kCT);
+        if constexpr (S::kQSmem) ptx::named_barrier_sync(2 + grp, 128);
 
         // The segment's state.
         float o[QB][MB][4];
@@ -308,7 +302,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
 #pragma unroll
                     for (int nb = 0; nb < QB; ++nb) {
                         if constexpr (S::kQSmem) {
-                            const uint4 f = ptx::ld_shared_v4(qfrag + ((nb * KW + i) * 32 + lane) * 16);
+                            const uint4 f = ptx::ld_shared_v4(qfrag + grp * S::kQgroup + ((nb * KW + i) * 32 + lane) * 16);
                             ptx::mma_f16_16816(sc[kb][nb], a, f.x, f.y);
                             ptx::mma_f16_16816(sc[kb][nb], c, f.z, f.w);
                         } else {
@@ -480,7 +474,7 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
             }
         };
 
-        for (; mine < it_end; mine += S::kGroups) {
+        for (; mine < it_end; mine += party.step()) {
             // On expiry the warp records the error and carries on with whatever
             // the stage holds (the call's output is then invalid): consumer
             // warps meet at named barriers, so none may leave the loop alone.
@@ -547,26 +541,27 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                         st[D + 1] = l[nb][h];
                     }
                 }
-            ptx::named_barrier_sync(1, S::kCT);
-            // Merge them in the order of the warps, and write the unit's output
-            // (this CTA saw all of it) or the CTA's partial.
+            party.sync();
+            // Merge the party's in the order of the warps, and write the unit's output
+            // (it saw all of it) or the part's partial.
             const size_t out_row0 = seg->row0;
             const uint32_t out_valid = seg->valid;
             const int unit = seg->unit;
             const bool sole = nseg == cur.nt;
             constexpr int C4 = D / 4;
-            for (int idx = tid; idx < S::kRows * C4; idx += S::kCT) {
+            const int rank = party.rank(tid), w0 = party.lead() * kTileWarps, w1 = party.end() * kTileWarps;
+            for (int idx = rank; idx < S::kRows * C4; idx += party.threads()) {
                 const int lr = idx / C4, c4 = idx - lr * C4;
                 if (!((out_valid >> lr) & 1u)) continue;
                 const float* st = obuf + lr * PS;
                 float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < S::kCW; ++w) M = fmaxf(M, st[w * S::kRows * PS + D]);
+#pragma unroll 4
+                for (int w = w0; w < w1; ++w) M = fmaxf(M, st[w * S::kRows * PS + D]);
                 const float Mu = M == -INFINITY ? 0.f : M;
                 float L = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < S::kCW; ++w) {
+#pragma unroll 4
+                for (int w = w0; w < w1; ++w) {
                     const float* sw = st + w * S::kRows * PS;
                     const float f = ptx::ex2(sw[D] - Mu);
                     const float4 v = reinterpret_cast<const float4*>(sw)[c4];
@@ -576,11 +571,11 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
                     acc.z = fmaf(v.z, f, acc.z);
                     acc.w = fmaf(v.w, f, acc.w);
                 }
-                write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + blockIdx.x, lr);
+                write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + party.part(), lr);
             }
             if (!sole && p.counters)
-                finish_unit<D, S::kRows>(p, unit, seg->unit_tile, cur.nt, N, P, out_row0, out_valid, tid, S::kCT, seg->flag);
-            ptx::named_barrier_sync(1, S::kCT);
+                finish_unit<D, S::kRows>(p, unit, seg->unit_tile, cur.nt, wp.total_tiles(), shares(wp), out_row0, out_valid, party, rank, segs[party.lead()].flag);
+            party.sync();
         }
         x += nseg;
         cur.j = cur.nt - 1;  // (the next unit; past the last one nothing reads it)
@@ -588,25 +583,27 @@ __global__ void __launch_bounds__(Q4Shape<D, QB>::kThreads, 1)
     }
 }
 
-template <int D, int QB, bool DP, bool TREE>
+template <int D, int QB, bool DP, bool TREE, bool SPLIT>
 cudaError_t launch_q4_t(const DecodeParams& p, int grid, cudaStream_t stream) {
     using S = Q4Shape<D, QB>;
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, QB, DP, TREE>,
+        cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, QB, DP, TREE, SPLIT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    cudaError_t e = launch_pdl(decode_q4_kernel<D, QB, DP, TREE>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);
+    cudaError_t e = launch_pdl(decode_q4_kernel<D, QB, DP, TREE, SPLIT>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 template <int D, int QB>
 cudaError_t launch_q4_shape(const DecodeParams& p, int grid, cudaStream_t stream) {
-    if (p.dplan) return p.anc ? cudaErrorInvalidValue : launch_q4_t<D, QB, true, false>(p, grid, stream);
-    return p.anc ? launch_q4_t<D, QB, false, true>(p, grid, stream) : launch_q4_t<D, QB, false, false>(p, grid, stream);
+    const bool split = p.num_ctas > grid;  // (never with a draft tree)
+    if (p.anc) return p.dplan || split ? cudaErrorInvalidValue : launch_q4_t<D, QB, false, true, false>(p, grid, stream);
+    if (split) return p.dplan ? launch_q4_t<D, QB, true, false, true>(p, grid, stream) : launch_q4_t<D, QB, false, false, true>(p, grid, stream);
+    return p.dplan ? launch_q4_t<D, QB, true, false, false>(p, grid, stream) : launch_q4_t<D, QB, false, false, false>(p, grid, stream);
 }
 
 }  // namespace

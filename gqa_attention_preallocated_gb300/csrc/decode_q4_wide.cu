@@ -35,39 +35,37 @@ using namespace q4;
 template <int QB>
 struct WideShape {
     static constexpr int D = 128;
-    static constexpr int kGroups = 3;                 // of four warps
-    // Blocks of 16 keys scored side by side, as many as the registers hold.
-    static constexpr int kChunks = QB == 4 ? 1 : 2;
+    // Groups of four warps: as many as leave a thread the registers it needs.
+    static constexpr int kGroups = q4_groups(D, 8 * QB);
     static constexpr int kCW = kGroups * kTileWarps;
     static constexpr int kCT = kCW * 32;
     static constexpr int kThreads = kCT + 128;        // a warpgroup copies (a warp a group of the others)
-    // Registers of a computing and of a copying thread after the split:
-    // 384 x 160 + 128 x 32 = 512 x 128, what they have at launch.
-    static constexpr int kRegs = 160, kCopyRegs = 32;
-    static_assert(kCT * kRegs + 128 * kCopyRegs <= 65536 && kThreads * 128 == 65536, "register split");
+    // Registers of a thread at launch, and of a computing and a copying one after
+    // the split: 384 x 160 + 128 x 32 = 512 x 128, or 256 x 232 + 128 x 40 = 384 x 168.
+    static constexpr int kLaunchRegs = kGroups == 3 ? 128 : 168;
+    static constexpr int kRegs = kGroups == 3 ? 160 : 232, kCopyRegs = kGroups == 3 ? 32 : 40;
+    static_assert(kCT * kRegs + 128 * kCopyRegs <= kThreads * kLaunchRegs && kThreads * kLaunchRegs <= 65536, "register split");
     static constexpr int kRows = 8 * QB;
     static constexpr int kStageB = Stage<D>::kBytes, kRowB = Stage<D>::kRowB, kCodeB = Stage<D>::kCodeB;
     static constexpr int kPS = D + 4;                 // floats of a partial's row: O, m, l, pad
     static constexpr int kPRow = kKT * 2 + 16;        // bytes of a weight row (the pad spreads 8 rows over all banks)
-    // Behind the stages: states [group][key half][row][kPS], weights [group][2][row],
-    // query fragments [QB][4 words][32 lanes] of 16 bytes, (sum of q, score factor) [row], each
-    // warp's maxima [group][warp][row] and exponents, sums l and the zero points'
-    // [group][warp][row], references of a group [group][row], sums set aside
-    // [block][thread].
-    static constexpr int kObuf = kGroups * kRows * kPS * 4;
-    static constexpr int kPhalf = kRows * kPRow;      // one tile's weights of a group; two of them
-    static constexpr int kPbuf = kGroups * 2 * kPhalf;
-    static constexpr int kSave = QB * kCT * 8;        // l set aside, 8 bytes a thread and block
+    // Behind the stages: for each group the weights of two tiles [2][row] and the
+    // sums l set aside [block][thread], at a segment's end its state [row][kPS];
+    // query fragments [group][QB][4 words][32 lanes] of 16 bytes, (sum of q, score
+    // factor) [group][row], each warp's maxima [group][warp][row] and exponents,
+    // sums l and the zero points' [group][warp][row], references [group][row].
+    static constexpr int kPhalf = kRows * kPRow;      // one tile's weights of a group
+    static constexpr int kTile = 2 * kPhalf + QB * 128 * 8, kState = kRows * kPS * 4;
+    static constexpr int kGroupB = kTile > kState ? kTile : kState;
     static constexpr int kQbuf = QB * 4 * 32 * 16;
-    static constexpr int kTile = kPbuf + kSave;       // (used within a segment, states only at its end)
-    static constexpr int kOffP = 0, kOffSave = kPbuf, kOffQ = kObuf > kTile ? kObuf : kTile, kOffQs = kOffQ + kQbuf, kOffMx = kOffQs + kRows * 8,
+    static constexpr int kOffQ = kGroups * kGroupB, kOffQs = kOffQ + kGroups * kQbuf, kOffMx = kOffQs + kGroups * kRows * 8,
                          kOffVe = kOffMx + kCW * kRows * 4, kOffLz = kOffVe + 64, kOffM = kOffLz + kCW * kRows * 8,
                          kMisc = kOffM + kGroups * kRows * 4;
     static constexpr int kFit = (232448 - 1024 - 512 - kMisc) / kStageB;
     static constexpr int kStages = kFit / kGroups * kGroups;
-    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kMisc + 2 * kStages * 8 + 16 + sizeof(Segment);
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageB + kMisc + 2 * kStages * 8 + 16 + kGroups * sizeof(Segment);
     static_assert(kStages >= 2 * kGroups, "a stage to read and one to fill for every group");
-    static_assert(kSmem <= 232448 && kMisc % 16 == 0 && kOffQ % 16 == 0 && kOffP % 16 == 0 && kOffLz % 8 == 0 && kOffSave % 16 == 0, "shared memory map");
+    static_assert(kSmem <= 232448 && kMisc % 16 == 0 && kGroupB % 16 == 0 && kOffLz % 8 == 0, "shared memory map");
 };
 
 // Barrier of a group's 128 threads that also ORs one bit.
@@ -82,27 +80,22 @@ __device__ __forceinline__ bool barrier_or(int id, bool v) {
     return r != 0;
 }
 
-template <int QB, bool DP, bool TREE>
+template <int QB, bool DP, bool TREE, bool SPLIT>
 __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     decode_q4_wide_kernel(const __grid_constant__ DecodeParams p) {
     using S = WideShape<QB>;
     constexpr int D = S::D, kStages = S::kStages, PS = S::kPS;
-    constexpr int kChunks = S::kChunks;
+    constexpr int kChunks = kWarpKeys / 16;  // blocks of 16 keys, scored side by side
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* misc = smem + static_cast<size_t>(kStages) * S::kStageB;
-    float* obuf = reinterpret_cast<float*>(misc);
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc + S::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages);
-    volatile Segment* seg = reinterpret_cast<volatile Segment*>(bars + 2 * kStages + 2);
+    volatile Segment* segs = reinterpret_cast<volatile Segment*>(bars + 2 * kStages + 2);  // a group's
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Part<DP> wp{p};
-    long long N = DP ? 0 : wp.total_tiles();
-    long long P = gridDim.x;
-    int x0 = static_cast<int>(static_cast<long long>(blockIdx.x) * N / P);
-    int x1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * N / P);
 
     const uint32_t stage0 = ptx::smem_addr(smem), misc0 = ptx::smem_addr(misc);
     const uint32_t bar0 = ptx::smem_addr(bars);  // full[s] = bar0 + 8s, empty[s] = bar0 + 8(kStages + s)
@@ -117,29 +110,27 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     __syncthreads();
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
-    if (DP) {
-        if (p.dplan->skip) return;  // a rejected device-resident step: nothing is written
-        N = wp.total_tiles();
-        // (With the counters every CTA of a unit's range must have a tile: no more
-        // CTAs than tiles, as the host's plan has it.)
-        if (p.counters) P = min(P, max(N, 1ll));
-        const long long i = min(static_cast<long long>(blockIdx.x), P);
-        x0 = static_cast<int>(i * N / P);
-        x1 = static_cast<int>(min(i + 1, P) * N / P);
-    }
+    if (DP && p.dplan->skip) return;  // a rejected device-resident step: nothing is written
     zero_padded_queries<D, DP>(p, wp, tid, S::kThreads);
-    if (x0 >= x1) return;
+    const int grp = warp < S::kCW ? warp / kTileWarps : warp - S::kCW;
+    const Party<S::kGroups, SPLIT> party{grp};
+    int x0, x1;  // this party's tiles
+    {
+        const long long N = wp.total_tiles(), P = shares(wp), i = party.part();
+        x0 = static_cast<int>(min(i, P) * N / P), x1 = static_cast<int>(min(i + 1, P) * N / P);
+    }
 
     if (warp >= S::kCW) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kCopyRegs));
-        if (warp >= S::kCW + S::kGroups) return;
-        produce<D, kStages, S::kGroups, DP>(p, wp, x0, x1, warp - S::kCW, lane, stage0, bar0, abort_flag);
+        if (grp < S::kGroups && x0 < x1)
+            produce<D, kStages, DP>(p, wp, x0, x1, party, lane, stage0, bar0, abort_flag);
         return;
     }
 
     // ------------------------------------------------------------------ consumers
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
-    const int grp = warp / kTileWarps, gw = warp % kTileWarps;
+    if (x0 >= x1) return;
+    const int gw = warp % kTileWarps;
     const int kh = gw >> 1, dh = gw & 1;  // output: this warp's half of the keys and of the dims
     const int koff = gw * kWarpKeys;      // scores: its keys of a tile
     const int quad = lane & 3, g = lane >> 2;
@@ -147,19 +138,21 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
     const uint32_t kpiece = kg * S::kRowB + quad * 16;
     const uint32_t vpiece_a = (kh * 64 + va) * S::kRowB + dh * 32 + g * 4;
     const uint32_t vpiece_b = (kh * 64 + vb) * S::kRowB + dh * 32 + g * 4;
-    const uint32_t pbuf = misc0 + S::kOffP + grp * 2 * S::kPhalf;
+    const uint32_t pbuf = misc0 + grp * S::kGroupB;
     const uint32_t pstore = pbuf + g * S::kPRow + (2 * quad) * 2;  // + half, + block of rows, + key
     const uint32_t pload = pbuf + (lane & 7) * S::kPRow + (kh * 64 + (lane >> 3) * 8) * 2;
-    float2* qsum = reinterpret_cast<float2*>(misc + S::kOffQs);
+    float2* qsum = reinterpret_cast<float2*>(misc + S::kOffQs) + grp * S::kRows;
     float* mxbuf = reinterpret_cast<float*>(misc + S::kOffMx) + grp * kTileWarps * S::kRows;
     uint32_t* vebuf = reinterpret_cast<uint32_t*>(misc + S::kOffVe) + grp * kTileWarps;
     float2* lzbuf = reinterpret_cast<float2*>(misc + S::kOffLz);
     float* mbuf = reinterpret_cast<float*>(misc + S::kOffM);
-    float2* save = reinterpret_cast<float2*>(misc + S::kOffSave) + tid;
+    float2* save = reinterpret_cast<float2*>(misc + grp * S::kGroupB + 2 * S::kPhalf) + (tid & 127);
+    const uint32_t qfrag = misc0 + S::kOffQ + grp * S::kQbuf + lane * 16;
+    volatile Segment* seg = segs + grp;
 
     Cursor<DP, kKT> cur;
     cur.init(wp, x0);
-    int mine = grp, stage = grp, phase = 0;
+    int mine = party.first_tile(), stage = grp, phase = 0;
 
     for (int x = x0; x < x1;) {
         // One segment: this CTA's tiles of one unit.
@@ -182,7 +175,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
             lane_lim = (lane < S::kRows && r < p.R && t < nn) ? prior + t : -1;
         }
         const uint32_t valid = __ballot_sync(0xffffffffu, lane_lim >= 0);
-        if (tid == 0) {
+        if ((tid & 127) == 0) {
             seg->row0 = row0;
             seg->valid = valid;
             seg->unit_tile = x - j0;
@@ -192,10 +185,10 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
         // Query fragments (as in decode_q4.cu): warp nb writes block nb's, and its
         // rows' sums and score factors.
         {
-            if (warp < QB) {
+            if (gw < QB) {
                 const uint4* qrow = nullptr;
-                if ((valid >> (warp * 8 + g)) & 1u)
-                    qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + warp * 8 + g) * D + quad * 32);
+                if ((valid >> (gw * 8 + g)) & 1u)
+                    qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + gw * 8 + g) * D + quad * 32);
                 uint4 w[4];
                 uint32_t top = 0;
 #pragma unroll
@@ -221,15 +214,15 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                         const float t = (c & 1) ? 0.0625f : 1.f;
                         h[c] = ptx::pack_f16x2(a0 * t, a1 * t);
                     }
-                    *reinterpret_cast<uint4*>(misc + S::kOffQ + ((warp * 4 + i) * 32 + lane) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(misc + S::kOffQ + grp * S::kQbuf + ((gw * 4 + i) * 32 + lane) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 if (quad == 0)  // 2^-24 sum, and 2^(e - 141) 2^24 log2(e) / sqrt(d)
-                    qsum[warp * 8 + g] = make_float2(sum * 5.9604644775390625e-8f,
+                    qsum[gw * 8 + g] = make_float2(sum * 5.9604644775390625e-8f,
                                                      p.scale_log2 * __uint_as_float(static_cast<uint32_t>(min(254, e + 10)) << 23));
             }
-            ptx::named_barrier_sync(1, S::kCT);
+            ptx::named_barrier_sync(2 + grp, 128);
         }
 
         // The segment's state: O^T of this warp's keys and dims; the negative of
@@ -347,7 +340,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 }
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
-                    const uint4 f = ptx::ld_shared_v4(misc0 + S::kOffQ + ((nb * 4 + i) * 32 + lane) * 16);
+                    const uint4 f = ptx::ld_shared_v4(qfrag + (nb * 4 + i) * 512);
 #pragma unroll
                     for (int u = 0; u < kChunks; ++u) ptx::mma_f16_16816(sa[u][nb], a[u], f.x, f.y);
 #pragma unroll
@@ -358,7 +351,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
             for (int u = 0; u < kChunks; ++u) settle(full, key0 + 16 * u, kwa[u], vwa[u], sa[u], pst + u * 32);
         };
 
-        for (uint32_t half = 0; mine < it_end; mine += S::kGroups, half ^= S::kPhalf) {
+        for (uint32_t half = 0; mine < it_end; mine += party.step(), half ^= S::kPhalf) {
             // (On expiry as in decode_q4.cu: record it and carry on.)
             if (!ptx::mbar_try_wait(bar0 + 8 * stage, phase) &&
                 !ptx::mbar_wait_bounded(bar0 + 8 * stage, phase, *abort_flag ? 0ull : kWaitLimitNs)) {
@@ -372,7 +365,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
 
             bool moved = false;
 #pragma unroll
-            for (int nb = 0; nb < QB; ++nb) save[nb * S::kCT] = make_float2(l[nb][0], l[nb][1]);
+            for (int nb = 0; nb < QB; ++nb) save[nb * 128] = make_float2(l[nb][0], l[nb][1]);
             const uint32_t pst = pstore + half + koff * 2;
             const bool full = key0 + kWarpKeys - 1 <= min_lim && key0 > max_lo && (!TREE || key0 + kWarpKeys <= prior);
             // Once, and again with moved references where they do not stand (one
@@ -382,8 +375,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 ve = 0;
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) mx[nb][0] = mx[nb][1] = -INFINITY;
-#pragma unroll 1
-                for (int k = 0; k < kWarpKeys; k += 16 * kChunks) weigh(full, key0 + k, koff + k, sK, sS, pst + k * 2);
+                weigh(full, key0, koff, sK, sS, pst);
                 bool move = seen != kAll || ve > vexp;
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) move |= fmaxf(mx[nb][0], mx[nb][1]) > kLazyRescale;
@@ -394,7 +386,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 ve = __reduce_max_sync(0xffffffffu, ve);
 #pragma unroll
                 for (int nb = 0; nb < QB; ++nb) {
-                    const float2 v = save[nb * S::kCT];
+                    const float2 v = save[nb * 128];
                     l[nb][0] = v.x, l[nb][1] = v.y;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -485,9 +477,9 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
             }
         }
 
-        // The segment's end: the groups' states into shared memory (over the weights,
+        // The segment's end: the group's state into shared memory (over its weights,
         // once no warp reads them) in real units.
-        ptx::named_barrier_sync(1, S::kCT);
+        ptx::named_barrier_sync(2 + grp, 128);
         const float real = 0.015625f * __uint_as_float(vexp << 23);  // 2^(vexp - 133), as a product that stays normal
         // (Keys' second halves are added to the first.)
         if (kh == 1) ptx::named_barrier_sync(2 + grp, 128);
@@ -507,7 +499,7 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                     e[v] = o[nb][mb][c] * 16777216.f * real;
                     e[v + 2] = o[nb][mb][2 + c] * 1048576.f * real;
                 }
-                float4* d4 = reinterpret_cast<float4*>(obuf + (grp * S::kRows + lr) * PS + dh * 64 + g * 8);
+                float4* d4 = reinterpret_cast<float4*>(misc + grp * S::kGroupB) + lr * (PS / 4) + dh * 16 + g * 2;
                 if (kh == 1) {
                     const float4 u = d4[0], v = d4[1];
                     e[0] += u.x, e[1] += u.y, e[2] += u.z, e[3] += u.w;
@@ -521,74 +513,76 @@ __global__ void __launch_bounds__(WideShape<QB>::kThreads, 1)
                 }
             }
         if (kh == 0) ptx::named_barrier_sync(2 + grp, 128);
-        ptx::named_barrier_sync(1, S::kCT);
-        // Merge the groups in their order, and write the unit's output (this CTA
-        // saw all of it) or the CTA's partial.
+        party.sync();
+        // Merge the party's groups in their order, and write the unit's output (it
+        // saw all of it) or the part's partial.
         const size_t out_row0 = seg->row0;
         const uint32_t out_valid = seg->valid;
         const int unit = seg->unit;
         const bool sole = nseg == cur.nt;
         constexpr int C4 = D / 4;
-        for (int idx = tid; idx < S::kRows * C4; idx += S::kCT) {
+        const int rank = party.rank(tid);
+        for (int idx = rank; idx < S::kRows * C4; idx += party.threads()) {
             const int lr = idx / C4, c4 = idx - lr * C4;
             if (!((out_valid >> lr) & 1u)) continue;
-            float gl[S::kGroups], gz[S::kGroups], gm[S::kGroups], M = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < S::kGroups; ++i) {
-                gl[i] = gz[i] = 0.f;
+            // A group's sum, zero points' sum and reference.
+            auto sums = [&](int i, float& gl, float& gz) {
+                gl = gz = 0.f;
 #pragma unroll
                 for (int w = 0; w < kTileWarps; ++w) {
                     const float2 lz = lzbuf[(i * kTileWarps + w) * S::kRows + lr];
-                    gl[i] += lz.x;
-                    gz[i] += lz.y;
+                    gl += lz.x;
+                    gz += lz.y;
                 }
-                gm[i] = mbuf[i * S::kRows + lr];
-                if (gm[i] == -INFINITY && gl[i] != 0.f) gm[i] = 0.f;  // (a row whose every score is NaN keeps that)
-                M = fmaxf(M, gm[i]);
-            }
+                const float m = mbuf[i * S::kRows + lr];
+                return m == -INFINITY && gl != 0.f ? 0.f : m;  // (a row whose every score is NaN keeps that)
+            };
+            float M = -INFINITY, gl, gz;
+            for (int i = party.lead(); i < party.end(); ++i) M = fmaxf(M, sums(i, gl, gz));
             const float Mu = M == -INFINITY ? 0.f : M;
             float L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < S::kGroups; ++i) {
-                const float f = ptx::ex2(gm[i] - Mu);
-                const float4 u = reinterpret_cast<const float4*>(obuf + (i * S::kRows + lr) * PS)[c4];
-                L = fmaf(gl[i], f, L);
-                acc.x = fmaf(u.x - gz[i], f, acc.x);
-                acc.y = fmaf(u.y - gz[i], f, acc.y);
-                acc.z = fmaf(u.z - gz[i], f, acc.z);
-                acc.w = fmaf(u.w - gz[i], f, acc.w);
+            for (int i = party.lead(); i < party.end(); ++i) {
+                const float f = ptx::ex2(sums(i, gl, gz) - Mu);
+                const float4 u = reinterpret_cast<const float4*>(misc + i * S::kGroupB)[lr * (PS / 4) + c4];
+                L = fmaf(gl, f, L);
+                acc.x = fmaf(u.x - gz, f, acc.x);
+                acc.y = fmaf(u.y - gz, f, acc.y);
+                acc.z = fmaf(u.z - gz, f, acc.z);
+                acc.w = fmaf(u.w - gz, f, acc.w);
             }
-            write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + blockIdx.x, lr);
+            write_row<D>(p, out_row0 + lr, c4, acc, M, L, sole, unit + party.part(), lr);
         }
         if (!sole && p.counters)
-            finish_unit<D, S::kRows>(p, unit, seg->unit_tile, cur.nt, N, P, out_row0, out_valid, tid, S::kCT, seg->flag);
-        ptx::named_barrier_sync(1, S::kCT);
+            finish_unit<D, S::kRows>(p, unit, seg->unit_tile, cur.nt, wp.total_tiles(), shares(wp), out_row0, out_valid, party, rank, segs[party.lead()].flag);
+        party.sync();
         x += nseg;
         cur.j = cur.nt - 1;  // (the next unit; past the last one nothing reads it)
         if (x < x1) cur.advance(wp);
     }
 }
 
-template <int QB, bool DP, bool TREE>
+template <int QB, bool DP, bool TREE, bool SPLIT>
 cudaError_t launch_wide_t(const DecodeParams& p, int grid, cudaStream_t stream) {
     using S = WideShape<QB>;
     static bool attr_set = false;
     if (!attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(decode_q4_wide_kernel<QB, DP, TREE>,
+        cudaError_t e = cudaFuncSetAttribute(decode_q4_wide_kernel<QB, DP, TREE, SPLIT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    cudaError_t e = launch_pdl(decode_q4_wide_kernel<QB, DP, TREE>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);
+    cudaError_t e = launch_pdl(decode_q4_wide_kernel<QB, DP, TREE, SPLIT>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 template <int QB>
 cudaError_t launch_wide_qb(const DecodeParams& p, int grid, cudaStream_t stream) {
-    if (p.dplan) return p.anc ? cudaErrorInvalidValue : launch_wide_t<QB, true, false>(p, grid, stream);
-    return p.anc ? launch_wide_t<QB, false, true>(p, grid, stream) : launch_wide_t<QB, false, false>(p, grid, stream);
+    const bool split = p.num_ctas > grid;  // (never with a draft tree)
+    if (p.anc) return p.dplan || split ? cudaErrorInvalidValue : launch_wide_t<QB, false, true, false>(p, grid, stream);
+    if (split) return p.dplan ? launch_wide_t<QB, true, false, true>(p, grid, stream) : launch_wide_t<QB, false, false, true>(p, grid, stream);
+    return p.dplan ? launch_wide_t<QB, true, false, false>(p, grid, stream) : launch_wide_t<QB, false, false, false>(p, grid, stream);
 }
 
 }  // namespace

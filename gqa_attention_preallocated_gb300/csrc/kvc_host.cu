@@ -261,6 +261,7 @@ struct AttnPlan {
     bool generic = false;  // the call runs on the generic kernel
     int Hq = 0, G = 0, T = 0, R = 0;
     int mt = 0, RPB = 0, RB = 0, NB = 0, units = 0, ways = 1, part_rows = 0;
+    int parts = 0;  // split-KV: shares that the call's tiles are divided into, at most
     int splits = 1;  // generic kernel: CTAs per (row block, KV head, row)
     size_t ws_err = 0, ws_plan = 0, ws_partials = 0, ws_total = 0;
     // Least workspace the call runs with: the tensor-core path needs only the
@@ -310,8 +311,13 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
         pl->ws_plan = round_up(sizeof(DevicePlan), 256) + round_up(kMaxTreeQueries * sizeof(uint64_t), 256);
         pl->ways = c->dtype == KVC_Q4 ? 1 : decode_launch_shape(pl->mt, c->dtype == KVC_FP8_E4M3, c->d).ways;
         pl->part_rows = std::min(pl->R, pl->RPB);
+        // A share a CTA.  4-bit: with a unit or more for every SM a share a warp
+        // group, so that one group's units end while the others compute.
+        pl->parts = num_ctas;
+        if (c->dtype == KVC_Q4 && pl->units >= num_ctas)
+            pl->parts = std::min(kMaxCtas, num_ctas * q4_groups(c->d, pl->RPB));
         pl->ws_partials = tc_only ? 0
-                                  : static_cast<size_t>(pl->units + num_ctas) * pl->ways * pl->part_rows *
+                                  : static_cast<size_t>(pl->units + pl->parts) * pl->ways * pl->part_rows *
                                         (c->d + 4) * sizeof(float);
         pl->ws_min = pl->ws_err + pl->ws_plan + pl->ws_partials;
         if (pl->R > tc_min_rows(c) && tc_capable(c)) {
@@ -768,20 +774,21 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     if (tiles > 0x7fffffffll) return fail(KVC_ERR_ARG, "too many key tiles in one call");
     p.gstart[pl.NB] = static_cast<int>(tiles);
     p.total_tiles = static_cast<int>(tiles);
-    // At most one CTA per SM, and never more CTAs than tiles: then every CTA
-    // owns at least one tile, so the CTAs covering a unit's tiles are exactly
-    // the contiguous range cta_of(first tile) .. cta_of(last tile), all of
+    // At most one CTA per SM, and never more shares than tiles: then every
+    // share holds at least one tile, so those covering a unit's tiles are exactly
+    // the contiguous range share_of(first tile) .. share_of(last tile), all of
     // which contribute a partial.
-    const int grid = static_cast<int>(std::max(1ll, std::min<long long>(c->num_sms, tiles)));
-    p.num_ctas = grid;
+    const int parts = static_cast<int>(std::max(1ll, std::min<long long>(anc ? c->num_sms : pl.parts, tiles)));
+    const int grid = std::min(c->num_sms, parts);
+    p.num_ctas = parts;
 
     // Does any unit need the combine kernel?  A unit is written in full by the
-    // attention kernel when all its tiles fall in one CTA (CTA i owns tiles
-    // floor(iN/P) .. floor((i+1)N/P)-1, so tile x belongs to CTA
+    // attention kernel when all its tiles fall in one share (share i owns tiles
+    // floor(iN/P) .. floor((i+1)N/P)-1, so tile x belongs to share
     // ((x+1)P - 1) / N) and, when warps own whole tiles, it is one tile.
     bool need_combine = false;
     if (!p.counters) {
-        const long long N = tiles, P = grid;
+        const long long N = tiles, P = parts;
         for (int q = 0; q < pl.NB && !need_combine; ++q) {
             const int nt = (p.gstart[q + 1] - p.gstart[q]) / c->Hkv;
             if (nt == 0) continue;
@@ -830,10 +837,10 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         cp.ways = pl.ways;
         cp.part_rows = pl.part_rows;
         cp.total_tiles = p.total_tiles;
-        cp.num_ctas = grid;
+        cp.num_ctas = parts;
         for (int b = 0; b < c->B; ++b) cp.n_new[b] = n_new[b];
         for (int q = 0; q <= pl.NB; ++q) cp.gstart[q] = p.gstart[q];
-        for (int i = 0; i <= grid; ++i) cp.cta_start[i] = static_cast<int>(static_cast<long long>(i) * tiles / grid);
+        for (int i = 0; i <= parts; ++i) cp.cta_start[i] = static_cast<int>(static_cast<long long>(i) * tiles / parts);
         e = launch_combine_bf16(cp, stream);
         if (e != cudaSuccess) return cuda_fail(e, "split-KV combine launch");
         ++c->launches;
@@ -1640,7 +1647,7 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     pp.RB = pl.RB;
     pp.NB = pl.NB;
     pp.Hkv = c->Hkv;
-    pp.num_ctas = grid;
+    pp.num_ctas = pl.parts;
     pp.max_len = c->max_len;
     pp.window = c->window;
     pp.ring = c->ring ? 1 : 0;
@@ -1667,7 +1674,7 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     p.RB = pl.RB;
     p.NB = pl.NB;
     p.part_rows = pl.part_rows;
-    p.num_ctas = grid;
+    p.num_ctas = pl.parts;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c->d)));
     p.append_new = 1;
     p.k_new = k_new;
@@ -1703,7 +1710,7 @@ kvc_status kvc_decode_step(kvc_cache* c, int layer, const void* q, const void* k
     cp.NB = pl.NB;
     cp.ways = pl.ways;
     cp.part_rows = pl.part_rows;
-    cp.num_ctas = grid;
+    cp.num_ctas = pl.parts;
     e = launch_combine_bf16(cp, st);
     if (e != cudaSuccess) return cuda_fail(e, "split-KV combine launch");
     ++c->launches;

@@ -39,6 +39,30 @@ struct Segment {
 };
 static_assert(sizeof(Segment) == 32, "shared memory map");
 
+// Who works on a segment together.  Joint: the CTA's groups, tiles in turn.  Split
+// (more parts than CTAs): every group has tiles of its own, and one group's
+// segment ends while the others compute.  (Two kernels: with the choice made
+// inside one, long decodes ran 7 % slower.)
+template <int kGroups, bool split>
+struct Party {
+    int grp;
+    __device__ __forceinline__ int part() const { return split ? grp * gridDim.x + blockIdx.x : blockIdx.x; }
+    __device__ __forceinline__ int first_tile() const { return split ? 0 : grp; }
+    static __device__ __forceinline__ constexpr int step() { return split ? 1 : kGroups; }
+    static __device__ __forceinline__ constexpr int threads() { return split ? kTileWarps * 32 : kGroups * kTileWarps * 32; }
+    __device__ __forceinline__ int rank(int tid) const { return split ? tid % (kTileWarps * 32) : tid; }
+    __device__ __forceinline__ int lead() const { return split ? grp : 0; }  // the party's groups: lead() ..
+    __device__ __forceinline__ int end() const { return split ? grp + 1 : kGroups; }
+    __device__ __forceinline__ void sync() const { ptx::named_barrier_sync(split ? 2 + grp : 1, threads()); }
+};
+
+// Shares of the call's tiles.  (With the counters every share of a unit's range
+// must have a tile: no more shares than tiles, as the host's plan has it.)
+template <bool DP>
+__device__ __forceinline__ int shares(const Part<DP>& w) {
+    return DP && w.p.counters ? min(w.p.num_ctas, max(w.total_tiles(), 1)) : w.p.num_ctas;
+}
+
 // Key of row i (0 .. 7) of an 8-key block, a nibble each.
 template <int D>
 __device__ __forceinline__ int perm8(int i) {
@@ -107,7 +131,7 @@ __device__ __forceinline__ void zero_padded_queries(const DecodeParams& p, const
 }
 
 // Four dims of a query row's merged state: the output (row `row` of out, [B Hq T, d]),
-// or this CTA's partial.
+// or this part's partial.
 template <int D>
 __device__ __forceinline__ void write_row(const DecodeParams& p, size_t row, int c4, float4 acc, float M, float L, bool sole,
                                           int slot, int lr) {
@@ -128,32 +152,32 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, size_t row, int
     }
 }
 
-// The end of a unit of which this CTA saw a part: the last CTA to leave its
-// partial merges all of them, in the order of the CTAs, and writes the unit's
-// output.  Called by all `threads` consumer threads, after the partial's writes;
-// `flag` is two ints of shared memory.  unit = (group q, KV head kvh), us its
-// first tile of N, ntiles its tiles; P CTAs.  p.counters returns to zero.
-template <int D, int kRows>
+// The end of a unit of which this party saw a part: the last party to leave its
+// partial merges all of them, in the order of the parts, and writes the unit's
+// output.  Called by all the party's threads, after the partial's writes; `flag`
+// is two ints of its shared memory.  unit = (group q, KV head kvh), us its
+// first tile of N, ntiles its tiles; P parts.  p.counters returns to zero.
+template <int D, int kRows, int kGroups, bool kSplit>
 __device__ __forceinline__ void finish_unit(const DecodeParams& p, int unit, long long us, int ntiles, long long N, long long P,
-                                            size_t row0, uint32_t valid, int tid, int threads, volatile int* flag) {
+                                            size_t row0, uint32_t valid, const Party<kGroups, kSplit>& party, int rank, volatile int* flag) {
     constexpr int PS = D + 4, C4 = D / 4, kChunk = 8;
     __threadfence();
-    ptx::named_barrier_sync(1, threads);
-    if (tid == 0) {
-        // Tile x belongs to CTA ((x + 1) P - 1) / N.
+    party.sync();
+    if (rank == 0) {
+        // Tile x belongs to part ((x + 1) P - 1) / N.
         const int c0 = static_cast<int>(((us + 1) * P - 1) / N), c1 = static_cast<int>(((us + ntiles) * P - 1) / N);
         const bool last = atomicAdd(p.counters + unit, 1) == c1 - c0;
         flag[0] = last ? c1 - c0 + 1 : 0;
         flag[1] = c0;
         if (last) p.counters[unit] = 0;  // ready for the next call
     }
-    ptx::named_barrier_sync(1, threads);
+    party.sync();
     const int n = flag[0];
     if (n > 0) {
         __threadfence();
         const float* base = p.partials + static_cast<size_t>(unit + flag[1]) * p.part_rows * PS;
         const size_t step = static_cast<size_t>(p.part_rows) * PS;
-        for (int idx = tid; idx < kRows * C4; idx += threads) {
+        for (int idx = rank; idx < kRows * C4; idx += party.threads()) {
             const int lr = idx / C4, c4 = idx - lr * C4;
             if (!((valid >> lr) & 1u)) continue;
             const float* row = base + static_cast<size_t>(lr) * PS;
@@ -192,11 +216,11 @@ __device__ __forceinline__ void finish_unit(const DecodeParams& p, int unit, lon
     }
 }
 
-// One producer warp: the tiles x0 .. x1 - 1 of its group (`first_tile`-th, then
-// every kGroups-th), a stage each, lanes 0 .. 3 issuing a tile's copies of K, V
+// One producer warp: the tiles x0 .. x1 - 1 of its group (the party's first, then
+// every step-th), a stage each, lanes 0 .. 3 issuing a tile's copies of K, V
 // and their scale words side by side.
-template <int D, int kStages, int kGroups, bool DP>
-__device__ __forceinline__ void produce(const DecodeParams& p, const Part<DP>& wp, int x0, int x1, int first_tile,
+template <int D, int kStages, bool DP, int kGroups, bool kSplit>
+__device__ __forceinline__ void produce(const DecodeParams& p, const Part<DP>& wp, int x0, int x1, const Party<kGroups, kSplit>& party,
                                         int lane, uint32_t stage0, uint32_t bar0, volatile int* abort_flag) {
     using St = Stage<D>;
     Cursor<DP, kKT> cur;
@@ -205,7 +229,8 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const Part<DP>& w
     const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache);
     const uint32_t* words = is_v ? p.q4.v : p.q4.k;
     const uint32_t dst_off = is_scale ? 2 * St::kCodeB + (is_v ? kKT * 4 : 0) : (is_v ? St::kCodeB : 0);
-    int mine = first_tile, stage = mine, phase = 1;  // (the first round of stages is free)
+    const int step = party.step();
+    int mine = party.first_tile(), stage = party.grp, phase = 1;  // (the first round of stages is free)
     int issued = 0;
     bool stop = false;
     for (int x = x0; x < x1 && !stop;) {
@@ -219,9 +244,9 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const Part<DP>& w
         // next multiple of 4, which the unit's stride holds).  The row of the
         // next tile is looked up before this one's stage is waited for.
         int row = mine < it_end ? key_row(p, b, kvh, first + mine * kKT) : 0;
-        for (; mine < it_end; mine += kGroups) {
+        for (; mine < it_end; mine += step) {
             const int n = min(kKT, extent - (first + mine * kKT));
-            const int next = mine + kGroups < it_end ? key_row(p, b, kvh, first + (mine + kGroups) * kKT) : 0;
+            const int next = mine + step < it_end ? key_row(p, b, kvh, first + (mine + step) * kKT) : 0;
             const uint32_t full = bar0 + 8 * stage;
             if (!ptx::mbar_try_wait(bar0 + 8 * (kStages + stage), phase) &&
                 !ptx::mbar_wait_bounded(bar0 + 8 * (kStages + stage), phase, kWaitLimitNs)) {
@@ -260,7 +285,7 @@ __device__ __forceinline__ void produce(const DecodeParams& p, const Part<DP>& w
     // completed).
     constexpr int kOwn = kStages / kGroups;  // this warp's stages
     for (int i = max(0, issued - kOwn); i < issued; ++i) {
-        const int st = first_tile + i % kOwn * kGroups;
+        const int st = party.grp + i % kOwn * kGroups;
         if (!ptx::mbar_wait_bounded(bar0 + 8 * st, (i / kOwn) & 1, kWaitLimitNs)) {
             if (lane == 0) atomicExch(p.err, kDevTimeoutDrain);
             break;

@@ -541,6 +541,38 @@ def test_longer_decode(d, B, Hkv, G, L):
         assert torch.equal(a, p.c.gqa_attention(0, q, np.ones(B)))
 
 
+@pytest.mark.parametrize("d,G,T,page,window", [(128, 4, 1, 0, 0), (128, 4, 4, 0, 0), (128, 5, 4, 128, 0), (128, 8, 4, 0, 0),
+                                               (128, 3, 3, 0, 200), (64, 4, 1, 128, 0), (64, 4, 4, 0, 0), (64, 5, 4, 0, 0),
+                                               (64, 8, 4, 0, 0), (128, 8, 1, 0, 130)])
+def test_units_for_every_sm(d, G, T, page, window):
+    """Rows times KV heads at least the SMs (156 units): each warp group takes units of its own, of one tile to
+    seven; then device-resident steps, with every row, with few, and with none."""
+    B, Hkv = 39, 4
+    p = Pair(B, Hkv, d, 896, window=window, page=page, seed=d + G + T)
+    n = p.rng.integers(0, 860, size=B)
+    n[:4] = 0, 1, 128, 860
+    q, k, v = p.inputs(n, 860, 1)
+    p.c.append(0, k.cuda(), v.cuda(), n)
+    p.note(k, v, n)
+    some = np.where(np.arange(B) % 5 == 2, 0, p.rng.integers(1, T + 1, size=B))
+    out = p.step(some, G, T=T)
+    again = p.c.gqa_attention(0, p.last_q, some)
+    assert torch.equal(out, again) and torch.equal(out, p.c.gqa_attention(0, p.last_q, some))
+    ws = torch.zeros(p.c.workspace_bytes(Hkv * G, T), dtype=torch.uint8, device="cuda")
+    p.c.lens_to_device()
+    one = np.zeros(B, dtype=np.int64)
+    one[3] = 1
+    for n_new in (some, one, np.zeros(B, dtype=np.int64), np.minimum(some, 1)):
+        q, k, v = p.inputs(n_new, T, G)
+        out = torch.full_like(q, 7, device="cuda")
+        p.c.decode_step(0, q.cuda(), k.cuda(), v.cuda(), torch.as_tensor(n_new, dtype=torch.int32, device="cuda"), out, ws)
+        p.note(k, v, n_new)
+        assert p.c.device_status(ws) == 0
+        p.check_out(out, q, n_new, T)
+    p.c.lens_from_device()
+    p.check_store()
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("T,G,window", [(200, 3, 0), (40, 4, 0), (9, 4, 0), (150, 4, 3000)])
 def test_long_prefill(d, T, G, window):
