@@ -70,7 +70,7 @@ template <int D, int QB>
 struct Q4Shape {
     // Warp groups taking tiles in turn: as many as leave a thread the registers
     // it needs (128 with 12 consumer warps, 168 with 8).
-    static constexpr int kGroups = QB == 1 ? 3 : 2;
+    static constexpr int kGroups = q4_groups(D, 8 * QB);
     static constexpr int kCW = kGroups * kTileWarps;
     static constexpr int kCT = kCW * 32;
     static constexpr int kThreads = kCT + 32 * kGroups;  // a producer warp a group

@@ -58,7 +58,7 @@ constexpr int kMaxScaleHeads = 64;
 // Keys per split-KV tile of 4-bit caches.
 constexpr int kQ4KeyTile = 128;
 // Warp groups of a CTA of the 4-bit split-KV kernels: `rows` query rows a block.
-constexpr int q4_groups(int d, int rows) { return rows == 8 || (d == 128 && rows <= 24) ? 3 : 2; }
+constexpr int q4_groups(int d, int rows) { return rows == 8 || (d == 128 ? rows <= 24 : rows <= 16) ? 3 : 2; }
 
 // ---------------------------------------------------------------------------
 // In-place append: k_new/v_new [B, Hkv, T, d] -> cache rows lens[b] .. lens[b]+n_new[b]-1.
