@@ -84,8 +84,9 @@ namespace {
 // rows (2,855 against 2,484 GB/s at 32) and the tcgen05 kernel from 64 (2,524
 // against 1,670).
 // A 4-bit cache: the split-KV kernels unpack a tile once for up to 32 rows and
-// lead there (B = 64, S = 4096: 201 us at 32 rows against 246); two blocks of
-// 32 rows read it twice (361 us at 48 rows against 247).
+// lead there (B = 64, S = 4096: 174 us at 32 rows against 232); two blocks of
+// 32 rows read it twice (318 us at 48 rows against 233; d = 64: 130 against 174,
+// and 237 against 174).
 constexpr int kTcMinRows = 12;
 constexpr int kTcMinRowsFp8 = 32;
 constexpr int kTcMinRowsQ4 = 32;
@@ -312,7 +313,10 @@ kvc_status plan_shape(const kvc_cache* c, int Hq, int T, int num_ctas, AttnPlan*
         pl->ways = c->dtype == KVC_Q4 ? 1 : decode_launch_shape(pl->mt, c->dtype == KVC_FP8_E4M3, c->d).ways;
         pl->part_rows = std::min(pl->R, pl->RPB);
         // A share a CTA.  4-bit: with a unit or more for every SM a share a warp
-        // group, so that one group's units end while the others compute.
+        // group, so that one group's units end while the others compute (decode of
+        // 32 rows of 6144, 256 units: 46 us against 50; 128 rows of 1536: 51 against
+        // 64); with fewer a group would leave more partials than it saves (one row
+        // of 8192, 8 units: 26 us against 14).
         pl->parts = num_ctas;
         if (c->dtype == KVC_Q4 && pl->units >= num_ctas)
             pl->parts = std::min(kMaxCtas, num_ctas * q4_groups(c->d, pl->RPB));
@@ -500,7 +504,8 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         // Many query rows per KV head: tensor-core kernel, one CTA per piece.
         // Work items are (b, kvh, row block, pair of 128-row tiles): with
         // T >= 128, 128 positions of two query heads (mode 0); with T < 128 the
-        // G*T rows r = g*T + t of the KV head packed into 128-row tiles (mode 1),
+        // G*T rows r = g*T + t of the KV head packed into 128-row tiles (mode 1;
+        // with a 4-bit cache longer chunks too, where that is less work),
         // or all in one tile whose two TMEM buffers take alternate key tiles
         // (mode 2, G*T <= 128).  An item's key tiles cost its tile count each
         // (one in mode 2), plus a fixed start-up cost per CTA.  The launch order
@@ -529,7 +534,6 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         pp.G = pl.G;
         pp.T = pl.T;
         pp.max_len = c->max_len;
-        pp.mode = pl.T >= 128 ? 0 : (pl.R <= 128 ? 2 : 1);
         pp.fp8 = c->dtype == KVC_FP8_E4M3 ? 1 : 0;
         if (pp.fp8)
             for (int h = 0; h < c->Hkv; ++h) {
@@ -541,8 +545,6 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         pp.q4 = q4_scales(c, layer);
         pp.k_cache = static_cast<const uint8_t*>(c->k[layer]);
         pp.v_cache = static_cast<const uint8_t*>(c->v[layer]);
-        pp.ntb = pp.mode == 0 ? (pl.T + 127) / 128 : 1;
-        pp.npair = pp.mode == 0 ? (pl.G + 1) / 2 : (pl.R + 255) / 256;
         pp.window = c->window;
         pp.ring = c->ring ? 1 : 0;
         pp.pg = c->pg;
@@ -550,30 +552,48 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         for (int b = 0; b < c->B; ++b) {
             pp.prior[b] = static_cast<int>(lens[b] - n_new[b]);
             pp.n_new[b] = n_new[b];
-            for (int kvh = 0; kvh < c->Hkv && pp.mode != 0 && n_new[b] > 0; ++kvh) {
-                // Packed rows: the last key any row sees is prior + min(T, n_new) - 1,
-                // and the first key any row's window starts at is prior - W + 1 or later.
-                const int kmax = pp.prior[b] + std::min(pl.T, static_cast<int>(n_new[b])) - 1;
-                const int kfirst = c->window > 0 ? std::max(0, pp.prior[b] - c->window + 1) : 0;
-                for (int pr = 0; pr < pp.npair; ++pr) {
-                    const int code = (b * c->Hkv + kvh) * pp.npair + pr;
-                    const int cost = pp.mode == 2 ? 1 : std::min(2, (pl.R - pr * 256 + 127) / 128);
-                    items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(cost)});
-                }
-            }
-            for (int kvh = 0; kvh < c->Hkv && pp.mode == 0; ++kvh)
-                for (int tb = 0; tb < pp.ntb; ++tb) {
-                    const int t0 = tb * 128;
-                    if (t0 >= n_new[b]) continue;
-                    const int kmax = pp.prior[b] + std::min(t0 + 127, static_cast<int>(n_new[b]) - 1);
-                    // First key any query of the block sees: its first query's window start.
-                    const int kfirst = c->window > 0 ? std::max(0, pp.prior[b] + t0 - c->window + 1) : 0;
+        }
+        // The call's items in a mode, and their cost in units (with a start of 14 each).
+        auto plan_items = [&](int mode) {
+            items.clear();
+            pp.mode = mode;
+            pp.ntb = mode == 0 ? (pl.T + 127) / 128 : 1;
+            pp.npair = mode == 0 ? (pl.G + 1) / 2 : (pl.R + 255) / 256;
+            for (int b = 0; b < c->B; ++b) {
+                for (int kvh = 0; kvh < c->Hkv && mode != 0 && n_new[b] > 0; ++kvh) {
+                    // Packed rows: the last key any row sees is prior + min(T, n_new) - 1,
+                    // and the first key any row's window starts at is prior - W + 1 or later.
+                    const int kmax = pp.prior[b] + std::min(pl.T, static_cast<int>(n_new[b])) - 1;
+                    const int kfirst = c->window > 0 ? std::max(0, pp.prior[b] - c->window + 1) : 0;
                     for (int pr = 0; pr < pp.npair; ++pr) {
-                        const int code = ((b * c->Hkv + kvh) * pp.ntb + tb) * pp.npair + pr;
-                        items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(std::min(2, pl.G - 2 * pr))});
+                        const int code = (b * c->Hkv + kvh) * pp.npair + pr;
+                        const int cost = mode == 2 ? 1 : std::min(2, (pl.R - pr * 256 + 127) / 128);
+                        items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(cost)});
                     }
                 }
-        }
+                for (int kvh = 0; kvh < c->Hkv && mode == 0; ++kvh)
+                    for (int tb = 0; tb < pp.ntb; ++tb) {
+                        const int t0 = tb * 128;
+                        if (t0 >= n_new[b]) continue;
+                        const int kmax = pp.prior[b] + std::min(t0 + 127, static_cast<int>(n_new[b]) - 1);
+                        // First key any query of the block sees: its first query's window start.
+                        const int kfirst = c->window > 0 ? std::max(0, pp.prior[b] + t0 - c->window + 1) : 0;
+                        for (int pr = 0; pr < pp.npair; ++pr) {
+                            const int code = ((b * c->Hkv + kvh) * pp.ntb + tb) * pp.npair + pr;
+                            items.push_back({code, kfirst / 128, kmax / 128 + 1, tile_cost(std::min(2, pl.G - 2 * pr))});
+                        }
+                    }
+            }
+            long long cost = 0;
+            for (const WorkItem& it : items) cost += static_cast<long long>(it.nkt - it.kt0) * it.nh + 14;
+            return cost;
+        };
+        const long long cost = plan_items(pl.T >= 128 ? 0 : (pl.R <= 128 ? 2 : 1));
+        // A 4-bit cache's chunk may run packed too where that is less work: with an
+        // odd number of heads, or a last block of few positions (batch 3 of 4000
+        // tokens, 4 KV heads of 3: 333 queries 55 us against 68, 129 queries 44
+        // against 69; batch 4 of 8192, 8 KV heads of 1, 256 queries: 78 against 92).
+        if (c->dtype == KVC_Q4 && pp.mode == 0 && plan_items(1) * 20 >= cost * 19) plan_items(0);
         const size_t slot_bytes = static_cast<size_t>(2) * 128 * (c->d + 4) * sizeof(float);
         const long long slot_room =
             std::min<long long>(kMaxPrefillSlots, static_cast<long long>((ws_bytes - pl.ws_err - pl.ws_plan) / slot_bytes));

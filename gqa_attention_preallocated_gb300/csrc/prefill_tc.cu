@@ -12,7 +12,7 @@
 // tile staged in shared memory (each 64 KB K/V tile then feeds four
 // 128x128x128 MMAs):
 //   mode 0 (T >= 128): 128 positions of a pair of query heads of the group;
-//   mode 1 (T < 128): 128-row tiles of the G*T rows r = g*T + t of one KV
+//   mode 1 (T < 128; 4-bit caches: or where it is less work): 128-row tiles of the G*T rows r = g*T + t of one KV
 //          head, packed (in [B, Hq, T, d] they are consecutive rows);
 //   mode 2 (G*T <= 128): one packed tile; the two TMEM S/O buffers and the two
 //          softmax warpgroups take alternate key tiles, so one buffer's softmax
@@ -28,12 +28,13 @@
 // 4-bit caches (KVC_Q4; also d = 64): a tile's codes and scale words arrive by
 // untiled copies in raw slots, two for K and one for V, and four warps, a row a
 // thread, convert K, then V, into the f16 tiles the MMAs read (all four on one
-// tensor: two warps for each of K and V took 236 us where this takes 207, B = 64,
-// S = 4096, 64 rows, as a tile's conversion stands in the way of its products).
+// tensor: with bf16 operands two warps for each of K and V took 236 us, this 207, B =
+// 64, S = 4096, 64 rows, as a tile's conversion stands in the way of its products).
 // The operands are f16, whose 11 bits keep s * (c - z) (at most 12) nearly whole
 // where bf16 would round it to 8: the error of a chunk's output against 64 bits
-// is 0.0018 so, 0.0034 with bf16 rows and weights, 0.0017 of it the output's own
-// rounding.  f16's range is met with powers of two: each tile's K and V by the
+// is 0.0017 so, that of the output's own rounding, and 0.0034 with bf16 rows and
+// weights, for 4 % more time (512 queries behind 12288 tokens, batch 4: 516 us,
+// 800 TFLOP/s, against 495; the queries' conversion and the tiles' exponents).  f16's range is met with powers of two: each tile's K and V by the
 // largest step among them (K's goes back into the tile's scores, V's into the
 // tile's weights, relative to a reference that moves with O when a tile's is
 // larger), each query row by its largest value.  c - z is exact in f16 and one

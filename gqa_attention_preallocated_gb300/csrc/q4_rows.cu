@@ -26,9 +26,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Rows of a thread: with long chunks four, whose loads are in flight together
-// (a prompt of 4 x 8192 tokens, d = 128: 1 and 4 rows measured, see the table
-// of operators); with few rows one, for more blocks.
+// Rows of a thread: with long chunks four, whose loads are in flight together and
+// whose divisions are one; with few rows one, for more blocks.  A prompt of 4 x
+// 8192 tokens, 8 heads, d = 128: appended in 33 us (46 with one row a
+// thread), read back in 26 (37).
 constexpr int kManyRows = 4;
 
 // LANES: lanes a row (a power of two, d / 8 or more of them: the others idle).

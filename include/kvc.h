@@ -28,9 +28,10 @@
  *   q, out                    [B, Hq, T, d]
  * All device pointers must be 16-byte aligned.  d * sizeof(element) must be a
  * multiple of 16, and d <= 256.  bf16 and FP8 caches of d = 128 run on the
- * TMA / tensor-core kernels.  fp32 caches, and bf16 or FP8 caches of any
+ * TMA / tensor-core kernels, 4-bit caches of d = 64 and 128 on kernels of
+ * their own.  fp32 caches, and bf16, FP8 or 4-bit caches of any
  * other d, run on a generic kernel.  That kernel widens the stored values to
- * fp32 (an FP8 code times its head's scale).  It has no fused append, no device-resident steps
+ * fp32 (an FP8 code times its head's scale, a 4-bit row's s * (c - z)).  It has no fused append, no device-resident steps
  * and no allocation-free entry point, and needs a workspace only for calls
  * whose key ranges it splits (kvc_workspace_bytes).
  *
@@ -174,7 +175,8 @@ kvc_status kvc_create_paged(kvc_cache** out, int layers, int batch, int kv_heads
  * [b][h][a] has s (bfloat16) in its high 16 bits and z in its low 16.  Other
  * producers may fill them (kvc_set_lens); of z the lowest 4 bits count.
  * head_dim is a multiple of 32, at most 256; all buffers
- * are 16-byte aligned.  q, k_new, v_new and out are bf16.
+ * are 16-byte aligned.  q, k_new, v_new and out are bf16; attention takes
+ * |q| < 2^112.
  *
  * Every call of this header serves such a cache as it serves an FP8 one, with
  * these limits: kvc_set_kv_scales does not apply; pages and rings of head_dim
@@ -223,7 +225,7 @@ kvc_status kvc_read(kvc_cache* c, int layer, const int64_t* first, const int32_t
 /* Bytes of device workspace kvc_gqa_attention needs for this handle, q_heads
  * and T (an error word and the split-KV partial results).
  * 0 means no workspace is needed: the generic kernel (fp32 caches; bf16 and
- * FP8 caches of d != 128) needs one only for calls with few (row, KV head,
+ * FP8 caches of d != 128; 4-bit caches of d other than 64 and 128) needs one only for calls with few (row, KV head,
  * 16-row block) units, whose key ranges it splits across CTAs.  Returns 0 for invalid
  * input. */
 size_t kvc_workspace_bytes(const kvc_cache* c, int q_heads, int T);
@@ -318,13 +320,14 @@ kvc_status kvc_host_copies_done(kvc_cache* c, void* stream);
  * a latency-critical loop that must not pay cudaMalloc's cost and implicit
  * synchronization.  The pages have no counterpart of this entry point; it
  * computes exactly what kvc_gqa_attention computes (same kernel, same
- * result) and serves bf16 and FP8 caches of d = 128.
+ * result) and serves bf16 and FP8 caches of d = 128, and 4-bit caches of d = 64
+ * and 128.
  *
  * Its scratch is one static device array of KVC_NOALLOC_SCRATCH_BYTES
  * (32 MiB) inside the library: every GPU that loads the library holds it
  * until the process exits.  No cudaMalloc, cudaFree or other allocating
  * call is made.  Calls with more than 12 query rows per KV head (G * T; 32
- * for FP8 caches) run on the tensor-core kernel, which needs only the workspace header and
+ * for FP8 and 4-bit caches) run on the tensor-core kernel, which needs only the workspace header and
  * uses the rest of the array for the partials of the items it cuts; they
  * always fit.  A call with fewer rows per KV head whose split-KV
  * scratch would exceed the array (very large batches; kvc_workspace_bytes
@@ -370,7 +373,7 @@ kvc_status kvc_noalloc_status(void* stream, int32_t* code);
  * kvc_truncate may only go back to a length n whose window keys
  * n - window + 1 .. n - 1 are still stored (or to 0).
  * Requirements: ring needs 1 <= window <= max_len and, for bf16 and FP8
- * caches of d = 128 and bf16 caches of d = 64, max_len % 128 == 0 (a key
+ * caches of d = 128, bf16 caches of d = 64 and 4-bit caches of both, max_len % 128 == 0 (a key
  * tile never wraps); ring storage changes only while every length is 0.
  * Applies to every layer and to every later call (including
  * kvc_decode_step).  Host only.  KVC_ERR_ARG otherwise. */
@@ -452,7 +455,8 @@ kvc_status kvc_lens_from_device(kvc_cache* c, void* stream);
  * rows per KV head (decode and short verify); 4-bit caches of d = 64 and 128
  * with G * T <= 32.
  * Three kernels are enqueued (device plan, attention with the append fused
- * in, combine), with nothing read from the host that changes per step, so
+ * in, combine; a 4-bit cache's attention merges its own units, but for very
+ * large batches), with nothing read from the host that changes per step, so
  * the call can be captured in a CUDA graph and replayed with new contents of
  * q, k_new, v_new and n_new.  The workspace is the one kvc_workspace_bytes
  * sizes (plus its device plan region, included there).

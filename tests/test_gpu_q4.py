@@ -589,6 +589,26 @@ def test_long_prefill(d, T, G, window):
             assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,T,window", [(3, 130, 0), (1, 260, 0), (5, 200, 90), (4, 129, 0)])
+def test_long_ragged_chunks_of_packed_rows(d, G, T, window):
+    """Chunks of 128 queries and more whose heads' rows share tiles; what stands in padded queries does not matter."""
+    p = Pair(4, 2, d, 700, window=window, seed=d + T)
+    p.step([300, 0, 257, 400], G, T=400)
+    n_new = [T, T - 3, 0, 70]
+    q, k, v = p.inputs(n_new, T, G)
+    for b in range(4):
+        for x in (q, k, v):
+            x[b, :, n_new[b]:] = float("nan")
+    out = p.c.append_attention(0, q.cuda(), k.cuda(), v.cuda(), n_new)
+    p.note(k, v, n_new)
+    for b in range(4):
+        assert not out[b, :, n_new[b]:].any()
+        q[b, :, n_new[b]:] = 0
+    p.check_out(out, q, n_new, T)
+    p.check_store()
+
+
 def test_streams_and_two_caches():
     """Calls of two caches on two streams at once, each with its own workspace."""
     a, b = Pair(2, 2, 128, 600, seed=1), Pair(2, 2, 64, 600, seed=2)
