@@ -24,7 +24,7 @@
 // block of 8 rows.
 //
 // Measured, 64 rows of 4096 tokens, 8 KV heads (287 MB): 16 query rows 107 us, 24
-// rows 133, 32 rows 174 (the tensor-core kernel: 232).  Bound by issue and its
+// rows 133, 32 rows 174 (the tensor-core kernel: 218).  Bound by issue and its
 // waits, not by a pipe: of the cycles 40 % issue, 35 % have the tensor pipe busy.
 // So warps count: the copying warps give up registers, and 24 rows ran 151 us with
 // two groups of 232 registers, 138 with three of 160; 32 rows 182 with three

@@ -84,9 +84,9 @@ namespace {
 // rows (2,855 against 2,484 GB/s at 32) and the tcgen05 kernel from 64 (2,524
 // against 1,670).
 // A 4-bit cache: the split-KV kernels unpack a tile once for up to 32 rows and
-// lead there (B = 64, S = 4096: 174 us at 32 rows against 232); two blocks of
-// 32 rows read it twice (318 us at 48 rows against 233; d = 64: 130 against 174,
-// and 237 against 174).
+// lead there (B = 64, S = 4096: 174 us at 32 rows against 218); two blocks of
+// 32 rows read it twice (318 us at 48 rows against 218; d = 64: 130 against 165,
+// and 237 against 165).
 constexpr int kTcMinRows = 12;
 constexpr int kTcMinRowsFp8 = 32;
 constexpr int kTcMinRowsQ4 = 32;

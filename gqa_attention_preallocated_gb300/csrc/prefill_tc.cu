@@ -33,8 +33,12 @@
 // The operands are f16, whose 11 bits keep s * (c - z) (at most 12) nearly whole
 // where bf16 would round it to 8: the error of a chunk's output against 64 bits
 // is 0.0017 so, that of the output's own rounding, and 0.0034 with bf16 rows and
-// weights, for 4 % more time (512 queries behind 12288 tokens, batch 4: 516 us,
-// 800 TFLOP/s, against 495; the queries' conversion and the tiles' exponents).  f16's range is met with powers of two: each tile's K and V by the
+// weights, for 4 % more time (the queries' conversion and the tiles' exponents).
+// Measured: 512 queries behind 12288 tokens, batch 4, 8 KV heads of 4: 451 us, 915
+// TFLOP/s; the same behind 4096 157 us; verify of 64 rows of 4096 with 64 query
+// rows 218 us.  Bound by the softmax warps' turn between two products (TMEM
+// loads waited for) and the start of each piece, which converts its first tiles
+// before anything can run.  f16's range is met with powers of two: each tile's K and V by the
 // largest step among them (K's goes back into the tile's scores, V's into the
 // tile's weights, relative to a reference that moves with O when a tile's is
 // larger), each query row by its largest value.  c - z is exact in f16 and one
@@ -160,7 +164,12 @@ struct RawRow {
         other = is_v ? k : v;
     }
     // ex: exponent field of the tile's largest step; values are s (c - z) 2^(137 - ex).
-    __device__ __forceinline__ void convert(uint8_t* tile, int r, bool is_v, int ex) const {
+    // kShort: code of a fourth the size.  The converters', the softmax's and the
+    // issuer's code pass one instruction cache, and with two row tiles that size is
+    // worth 2 to 10 %; with one, conversion is what the products wait for, and its
+    // own speed counts (64 query rows: 218 us unrolled, 245 short).
+    template <bool kShort>
+    __device__ __forceinline__ void convert(uint8_t* tile, int r, bool is_v, int ex) {
         auto is_nan = [](uint32_t word) { return (word & 0x7FFF0000u) >= 0x7F800000u; };
         const float step = q4::step_of(own) * __uint_as_float(static_cast<uint32_t>(264 - ex) << 23);
         uint32_t s = ptx::pack_f16x2(step, step);
@@ -170,10 +179,13 @@ struct RawRow {
             s = 0x7E007E00u;
         }
         const uint32_t z = 0x64006400u + (own & 15u) * 0x00010001u;  // 1024 + z, twice
-#pragma unroll
+        constexpr int kUnroll = kShort ? 1 : kPieces;
+#pragma unroll kUnroll
         for (int i = 0; i < kPieces; ++i) {
             const int piece = (i + (r >> 1)) % kPieces;
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int n = 0; n + 1 < kPieces; ++n) w[n] = w[n + 1];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // word k: columns 32 piece + 8k .. + 7
                 uint32_t o[4];
@@ -196,21 +208,20 @@ template <int kDim>
 __device__ __forceinline__ float convert_query_row(uint8_t* tile, int r) {
     constexpr int kChunks = kDim / 8;
     auto chunk = [&](int c) { return reinterpret_cast<uint4*>(tile + (c >> 3) * kBoxBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
-    uint4 v[kChunks];
     uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) v[c] = *chunk(c);
-#pragma unroll
+#pragma unroll 8
     for (int c = 0; c < kChunks; ++c) {
-        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        const uint4 v = *chunk(c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
     }
     const int e = max(16, static_cast<int>(top >> 7));
     const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);  // 2^(141 - e)
-#pragma unroll
+#pragma unroll 4
     for (int c = 0; c < kChunks; ++c) {
-        uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        const uint4 v = *chunk(c);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = ptx::pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xFFFF0000u) * f);
         *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -818,7 +829,7 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(kBarRawEmpty + sl));
             if (j >= 2) wait_for((is_v ? kBarVEmpty : kBarKEmpty) + s, ((j >> 1) & 1) ^ 1);  // the MMAs have read tile j - 2
-            row.convert(smem + (is_v ? kOffV : kOffK) + s * kTile128, r, is_v, is_v ? ev : ek);
+            row.template convert<!kAlt>(smem + (is_v ? kOffV : kOffK) + s * kTile128, r, is_v, is_v ? ev : ek);
             arrive((is_v ? kBarVFull : kBarKFull) + s);
         };
         wait_for(kBarQRaw, 0);
@@ -1042,27 +1053,35 @@ __global__ void __launch_bounds__(threads_pf(kFmt), 1)
                 const uint64_t sc2 = f2pack(sl2, sl2), nmu2 = f2pack(add, add);
                 uint64_t sum2 = f2pack(0.f, 0.f);
                 uint32_t pk[32];
+                // (4-bit: a copy of the code for tiles without masks, whose every
+                // element would test for them: 451 us where one copy took 507, 512
+                // queries behind 12288 tokens, batch 4.)
+                auto weights = [&](auto tag) {
+                    constexpr bool masked = decltype(tag)::value;
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    tmem_ld64(tS + c * 64, v);
-                    tmem_ld_wait();
-                    const int kl = full_tile ? 1 << 30 : lim - key0 - c * 64;
-                    const int kll = (full_tile || !kWin) ? -1 : lo_row - key0 - c * 64;
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld64(tS + c * 64, v);
+                        tmem_ld_wait();
+                        const int kl = full_tile ? 1 << 30 : lim - key0 - c * 64;
+                        const int kll = (full_tile || !kWin) ? -1 : lo_row - key0 - c * 64;
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        float x0, x1;
-                        f2unpack(ffma2(f2pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nmu2), x0, x1);
-                        float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-                        if (!full_tile) {
-                            if (e > kl || e <= kll) p0 = 0.f;
-                            if (e + 1 > kl || e + 1 <= kll) p1 = 0.f;
+                        for (int e = 0; e < 64; e += 2) {
+                            float x0, x1;
+                            f2unpack(ffma2(f2pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sc2, nmu2), x0, x1);
+                            float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+                            if (masked && !full_tile) {
+                                if (e > kl || e <= kll) p0 = 0.f;
+                                if (e + 1 > kl || e + 1 <= kll) p1 = 0.f;
+                            }
+                            sum2 = fadd2(sum2, f2pack(p0, p1));
+                            pk[e >> 1] = kF8 || kQ4 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
                         }
-                        sum2 = fadd2(sum2, f2pack(p0, p1));
-                        pk[e >> 1] = kF8 || kQ4 ? ptx::pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+                        // keys c*64 .. c*64+63 -> P columns c*32 .. c*32+31 (S columns already read)
+                        tmem_st32(tS + c * 32, pk);
                     }
-                    // keys c*64 .. c*64+63 -> P columns c*32 .. c*32+31 (S columns already read)
-                    tmem_st32(tS + c * 32, pk);
-                }
+                };
+                if (kQ4 && full_tile) weights(std::false_type());
+                else weights(std::true_type());
                 {
                     float s0, s1;
                     f2unpack(sum2, s0, s1);
