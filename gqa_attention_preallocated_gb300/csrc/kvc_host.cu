@@ -553,7 +553,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
             pp.prior[b] = static_cast<int>(lens[b] - n_new[b]);
             pp.n_new[b] = n_new[b];
         }
-        // The call's items in a mode, and their cost in units (with a start of 14 each).
+        // The call's items in a mode, and their cost in units (with a start of 18 each).
         auto plan_items = [&](int mode) {
             items.clear();
             pp.mode = mode;
@@ -585,7 +585,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                     }
             }
             long long cost = 0;
-            for (const WorkItem& it : items) cost += static_cast<long long>(it.nkt - it.kt0) * it.nh + 14;
+            for (const WorkItem& it : items) cost += static_cast<long long>(it.nkt - it.kt0) * it.nh + 18;
             return cost;
         };
         const long long cost = plan_items(pl.T >= 128 ? 0 : (pl.R <= 128 ? 2 : 1));
@@ -620,13 +620,16 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
                 // A 4-bit cache's items cost more to start (the first tiles wait for
                 // their conversion) and more a tile with one row tile (the
                 // conversion serves one and not two): 3 and 4 units a tile, start-up
-                // 14.  With fewer items than SMs its pieces may be of 4 tiles, as
-                // blocks of many pieces are merged by a launch of their own (333
-                // queries of 3 heads behind 4000 tokens: 78 us with the units above
-                // and pieces of 8, 61 with these; with more items than SMs pieces of
-                // 4 were 3 % slower).
+                // 18.  With fewer items than SMs its pieces may be of 4 tiles, as
+                // blocks of many pieces are merged by a launch of their own (with
+                // the units above and pieces of 8 against these: 333 queries of 3
+                // heads behind 4000 tokens, batch 3, 59 us and 50; 100 queries of 4
+                // behind 15000, 2 KV heads, 68 and 39; with more items than SMs
+                // pieces of 4 were 3 % slower).  Start-ups of 10, 14, 18, 22 and 28:
+                // 512 queries behind 8192 98, 97, 87, 86 and 92 us, behind 12288,
+                // batch 4, 460, 452, 444, 445 and 438.
                 const bool q4 = c->dtype == KVC_Q4;
-                const long long kStartCost = q4 ? 14 : 5;
+                const long long kStartCost = q4 ? 18 : 5;
                 const int kMinPieceTiles = q4 && n_items < nsm ? 4 : 8;
                 long long W = 0;
                 for (size_t k = i0; k < i1; ++k)

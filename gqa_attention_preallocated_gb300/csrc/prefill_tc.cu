@@ -34,7 +34,7 @@
 // where bf16 would round it to 8: the error of a chunk's output against 64 bits
 // is 0.0017 so, that of the output's own rounding, and 0.0034 with bf16 rows and
 // weights, for 4 % more time (the queries' conversion and the tiles' exponents).
-// Measured: 512 queries behind 12288 tokens, batch 4, 8 KV heads of 4: 451 us, 915
+// Measured: 512 queries behind 12288 tokens, batch 4, 8 KV heads of 4: 444 us, 928
 // TFLOP/s; the same behind 4096 157 us; verify of 64 rows of 4096 with 64 query
 // rows 218 us.  Bound by the softmax warps' turn between two products (TMEM
 // loads waited for) and the start of each piece, which converts its first tiles

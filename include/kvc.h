@@ -263,8 +263,8 @@ kvc_status kvc_append_attention(kvc_cache* c, int layer, const void* q, const vo
  * sees every key before the chunk plus the chunk's tokens on its own path to
  * the root (itself and its ancestors) instead of the triangle; everything
  * else is as in kvc_gqa_attention / kvc_append_attention.  Limits: T <= 64,
- * B * T <= 1024, no sliding window; bf16 caches take G * T <= 64 query rows
- * per KV head.  Errors (nothing enqueued): those of the plain calls, and
+ * B * T <= 1024, no sliding window; bf16 caches, and 4-bit ones of d = 64 and 128, take
+ * G * T <= 64 query rows per KV head.  Errors (nothing enqueued): those of the plain calls, and
  * KVC_ERR_SHAPE for a parent outside -1 .. t-1 or a shape past the limits,
  * KVC_ERR_ARG for a null parents or a cache with a window. */
 kvc_status kvc_gqa_attention_tree(kvc_cache* c, int layer, const void* q, int q_heads, int T,
