@@ -760,7 +760,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
         p.anc = dev_anc;
     }
     p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(c->d)));
-    long long tiles = 0;
+    long long tiles = 0, live_units = 0;
     for (int b = 0; b < c->B; ++b) {
         p.prior[b] = static_cast<int>(lens[b] - n_new[b]);
         p.n_new[b] = n_new[b];
@@ -791,6 +791,7 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
             const int first_tile = kfirst / kt;
             const int ntiles = extent > 0 ? (extent - 1) / kt + 1 - first_tile : 0;
             p.gstart[b * pl.RB + rb] = static_cast<int>(tiles);
+            if (ntiles > 0) live_units += c->Hkv;
             tiles += static_cast<long long>(ntiles) * c->Hkv;
         }
     }
@@ -801,7 +802,9 @@ kvc_status do_attention(kvc_cache* c, int layer, const void* q, const AttnPlan& 
     // share holds at least one tile, so those covering a unit's tiles are exactly
     // the contiguous range share_of(first tile) .. share_of(last tile), all of
     // which contribute a partial.
-    const int parts = static_cast<int>(std::max(1ll, std::min<long long>(anc ? c->num_sms : pl.parts, tiles)));
+    // (A share a group only if units enough have tiles, and never with a tree.)
+    const int most = anc || live_units < c->num_sms ? c->num_sms : pl.parts;
+    const int parts = static_cast<int>(std::max(1ll, std::min<long long>(most, tiles)));
     const int grid = std::min(c->num_sms, parts);
     p.num_ctas = parts;
 

@@ -558,6 +558,8 @@ def test_units_for_every_sm(d, G, T, page, window):
     out = p.step(some, G, T=T)
     again = p.c.gqa_attention(0, p.last_q, some)
     assert torch.equal(out, again) and torch.equal(out, p.c.gqa_attention(0, p.last_q, some))
+    few = np.where(np.arange(B) % 9 == 1, T, 0)  # (units with tiles are fewer than the SMs: the groups work together)
+    p.step(few, G, T=T)
     ws = torch.zeros(p.c.workspace_bytes(Hkv * G, T), dtype=torch.uint8, device="cuda")
     p.c.lens_to_device()
     one = np.zeros(B, dtype=np.int64)
@@ -587,6 +589,40 @@ def test_long_prefill(d, T, G, window):
         for _ in range(3):
             again = p.c.gqa_attention(0, p.last_q, n_new)
             assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("d,G,T", [(64, 4, 1), (128, 4, 1), (128, 4, 4), (64, 4, 4)])
+def test_more_units_than_the_workspace_counts(d, G, T):
+    """9000 units: the separate merge, with units for every SM and with a few; host and device plans."""
+    rows, Hkv, L = 20, 9, 300
+    p = Pair(rows, Hkv, d, L + 20, seed=d + T)
+    n = p.rng.integers(L // 2, L + 1, size=rows)
+    q, k, v = p.inputs(n, L, 1)
+    p.c.append(0, k.cuda(), v.cuda(), n)
+    p.note(k, v, n)
+    big = KVCache(1, 1000, Hkv, L + 20, d, dtype="q4")
+    for to, src in ((big.k, p.c.k), (big.v, p.c.v), (big.k_scale, p.c.k_scale), (big.v_scale, p.c.v_scale)):
+        to[0][:rows].copy_(src[0])
+    big.set_lens(0, np.concatenate([n, np.zeros(1000 - rows, dtype=np.int64)]))
+    assert big.B * big.Hkv > 8192
+    for live in (rows, 3):
+        n_new = np.where(np.arange(1000) < live, T, 0)
+        q = torch.zeros(1000, Hkv * G, T, d, dtype=torch.bfloat16)
+        q[:rows] = p.inputs(n_new[:rows], T, G)[0]
+        out = big.gqa_attention(0, q.cuda(), n_new)
+        assert not out[rows:].any() and big.device_status() == 0
+        p.check_out(out[:rows], q[:rows], n_new[:rows], T)
+    ws = torch.zeros(big.workspace_bytes(Hkv * G, T), dtype=torch.uint8, device="cuda")
+    big.lens_to_device()
+    q, k, v = (torch.zeros(1000, H, T, d, dtype=torch.bfloat16) for H in (Hkv * G, Hkv, Hkv))
+    n_new = np.where(np.arange(1000) < rows, T, 0)
+    for to, src in zip((q, k, v), p.inputs(n_new[:rows], T, G)):
+        to[:rows] = src
+    out = torch.full_like(q, 7, device="cuda")
+    big.decode_step(0, q.cuda(), k.cuda(), v.cuda(), torch.as_tensor(n_new, dtype=torch.int32, device="cuda"), out, ws)
+    p.note(k[:rows], v[:rows], n_new[:rows])
+    assert big.device_status(ws) == 0 and not out[rows:].any()
+    p.check_out(out[:rows], q[:rows], n_new[:rows], T)
 
 
 @pytest.mark.parametrize("d", [64, 128])
