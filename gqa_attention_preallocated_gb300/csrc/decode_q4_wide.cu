@@ -580,6 +580,12 @@ cudaError_t launch_wide_t(const DecodeParams& p, int grid, cudaStream_t stream) 
         cudaError_t e = cudaFuncSetAttribute(decode_q4_wide_kernel<QB, DP, TREE, SPLIT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
         if (e != cudaSuccess) return e;
+        // The registers that the computing warps take must be there at launch: with
+        // fewer they would wait for them for ever.
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, decode_q4_wide_kernel<QB, DP, TREE, SPLIT>);
+        if (e != cudaSuccess) return e;
+        if ((fa.numRegs + 7) / 8 * 8 < S::kLaunchRegs) return cudaErrorInvalidConfiguration;
         attr_set = true;
     }
     cudaError_t e = launch_pdl(decode_q4_wide_kernel<QB, DP, TREE, SPLIT>, dim3(grid), dim3(S::kThreads), S::kSmem, stream, p);

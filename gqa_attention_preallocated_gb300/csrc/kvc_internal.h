@@ -160,7 +160,7 @@ struct DecodeParams {
     int R, RPB, RB, NB;
     int part_rows;      // rows stored per partial sub-slot: min(R, RPB)
     int total_tiles;
-    int num_ctas;
+    int num_ctas;       // shares of the tiles: one a CTA, or (4-bit) one a warp group
     float scale_log2;   // log2(e) / sqrt(d)
     // In-kernel append (warps owning whole tiles only): when append_new is set
     // the chunk's rows k_new/v_new [B, Hkv, Tn, d] are written to the layer's
